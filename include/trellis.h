@@ -355,6 +355,184 @@ int trellis_probe_gateup_decode_free(const uint32_t* gcodes, const uint16_t* gsc
                                      const uint16_t* uscales, const uint16_t* x, uint16_t* out, int64_t R,
                                      int64_t C, int M, int k, int L, int T, void* stream);
 
+/*
+ * ---- attention between the projections ------------------------------------
+ *
+ * A decoder layer's projections leave queries, keys and values; the calls
+ * below take them through a paged key/value cache and back to the rows that
+ * the output projection reads: trellis_cache_reserve names the slots of new
+ * tokens, trellis_qk_norm_rope fills them, trellis_tree_attention or
+ * trellis_window_attention reads them, trellis_cache_accept keeps the
+ * accepted drafts, trellis_cache_fork and trellis_cache_free share and return
+ * pages.  These operators are this library's additions; the pages' decode
+ * verifies up to four rows at once (mlx-bun 0.2.0 -> 0.3.0 diff, page 42,
+ * src/model/qwen3_5.ts createAppend), which is what the tree form serves.
+ *
+ * trellis_kv_cache -- one paged cache.  A page holds P = page_size tokens of
+ * every key head.  The layouts are the operand order of the matrix units, 16
+ * bytes being 8 consecutive elements of the contraction:
+ *   k [layers, pages, heads, head_dim/8, P, 8]
+ *   v [layers, pages, heads, P/8, head_dim, 8]
+ * i.e. dimension d of token t (slot = page * P + t) is element
+ *   k: (((page * heads + h) * head_dim/8 + d/8) * P + t) * 8 + d%8
+ *   v: (((page * heads + h) * P/8 + t/8) * head_dim + d) * 8 + t%8
+ * of its layer.  dtype: TRELLIS_KV_BF16 or TRELLIS_KV_F16, also the type of
+ * every other 16-bit tensor of the call.  head_dim in {64, 128, 256};
+ * page_size a power of two, 16..256 (others: TRELLIS_EUNSUPPORTED).  The
+ * attention and append calls work on one layer (layers = 1, the pointers at
+ * that layer); the cache calls on all layers at once.  k and v are 16-byte
+ * aligned.
+ *
+ * trellis_kv_state -- the sequences' pages, in device memory:
+ *   table   int32 [seqs, width]  pages of each sequence in order, -1: none
+ *   lengths int32 [seqs]         cached tokens
+ *   refs    int32 [pages]        sequences that hold each page (0: free);
+ *                                only the cache calls read it
+ * The caller starts with table = -1, lengths = 0, refs = 0.  table, lengths
+ * and refs are 16-byte aligned; width * page_size below 2^31.
+ *
+ * Device-side contents are not seen by the host checks.  Every kernel bounds
+ * what it reads there: rows and pages outside the arrays are never touched,
+ * keys without storage are never seen, sequence numbers outside 0..seqs-1
+ * are skipped.
+ */
+#define TRELLIS_KV_BF16 0
+#define TRELLIS_KV_F16 1
+
+/* Most tokens of one sequence in a tree call, most drafted rows an accept
+ * call keeps, most sequences of one cache call. */
+#define TRELLIS_TREE_MAX 64
+#define TRELLIS_ACCEPT_MAX 64
+#define TRELLIS_CACHE_MAX_SEQS 1024
+
+typedef struct trellis_kv_cache {
+  uint16_t* k;
+  uint16_t* v;
+  int64_t pages;
+  int layers, heads, head_dim, page_size, dtype;
+} trellis_kv_cache;
+
+typedef struct trellis_kv_state {
+  int32_t* table;
+  int32_t* lengths;
+  int32_t* refs;
+  int64_t seqs, width;
+} trellis_kv_state;
+
+/*
+ * trellis_qk_norm_rope -- per-head RMS norm of queries and keys, rotation by
+ * position, and the append of keys and values to the cache, in one launch:
+ *   y = x / sqrt(mean(x^2) + eps) * weight          over each head
+ *   (a, b) -> (a cos t - b sin t, b cos t + a sin t) over the first
+ *   rotary_dim dimensions, t = positions[n] * inv_freq[i]; pair i is
+ *   (i, i + rotary_dim/2), or (2i, 2i + 1) when interleaved.
+ * All in f32 (the angle in f64), rounded once.
+ *   q [tokens, heads_q, head_dim], rows q_stride elements apart (heads of a
+ *   row contiguous); k, v [tokens, cache->heads, head_dim] likewise: the three
+ *   may be views of one projection output.  Strides are multiples of 8.
+ *   q_weight, k_weight [head_dim];  inv_freq f32 [rotary_dim/2]
+ *   positions int32 [tokens];  slots int32 [tokens]: page * page_size + offset;
+ *   a token whose slot is outside the cache (-1) is normed and rotated, and
+ *   not cached.  Two tokens must not share a slot.
+ *   out [tokens, heads_q, head_dim], contiguous
+ *   rotary_dim: a multiple of 16, 0..head_dim (inv_freq may be NULL at 0).
+ * tokens = 0 is no work and no error (also for the attention calls).
+ */
+int trellis_qk_norm_rope(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                         int64_t v_stride, const uint16_t* q_weight, const uint16_t* k_weight,
+                         const int32_t* positions, const float* inv_freq, int rotary_dim, int interleaved, float eps,
+                         const int32_t* slots, uint16_t* out, const trellis_kv_cache* cache, int64_t tokens,
+                         int heads_q, void* stream);
+
+/*
+ * trellis_tree_attention -- attention of drafted tokens over the cache and
+ * their own ancestors: out = softmax(scale q k^T) v per head, query head h
+ * reading key head h / (heads_q / cache->heads).
+ * Entry e (of n) is sequence seq_ids[e] (seq_ids NULL: sequence e) with the
+ * rows q_start[e] .. q_start[e+1]-1 of q; its token i sits in cache slot
+ * lengths + i of the sequence (written before the call).  Token i sees all
+ * lengths cached tokens and the entry's tokens m whose bit m is set in
+ * ancestors[row] (a token that is to see itself has its own bit set); bits
+ * without a token are ignored.  One token with mask 1 is plain decoding.  A
+ * row that sees nothing gives zeros.  Infinities and NaN in tokens that a row
+ * does not see do not reach it.
+ *   q [tokens, heads_q, head_dim], rows q_stride elements apart (a multiple of 8)
+ *   q_start int32 [n+1] ascending;  ancestors int64 [tokens] (bit masks)
+ *   max_q: the most tokens of any entry, 1..TRELLIS_TREE_MAX; rows past it
+ *   in an entry, and rows of unknown sequences, are not written
+ *   out [tokens, heads_q, head_dim] contiguous, 16-byte aligned
+ *   scale: finite, > 0
+ * Scores, softmax and sums are f32; weights are rounded once to the cache's
+ * type before they multiply the values.  Results do not depend on timing:
+ * the same call gives the same bits.
+ *
+ * trellis_window_attention -- the same for consecutive tokens: token i, at
+ * position p = lengths + i, sees the keys j <= p with p - j < window or
+ * j < sinks.  window = 0: all j <= p.  max_q >= 1 has no upper bound.  Any
+ * number of tokens: single-token decoding and prompt chunks.
+ *
+ * The workspace holds the partial results of keys that are split over
+ * workgroups; the size queries take the call's sizes.
+ */
+size_t trellis_tree_attention_workspace_bytes(const trellis_kv_cache* cache, const trellis_kv_state* state, int n,
+                                              int64_t tokens, int heads_q, int max_q);
+int trellis_tree_attention(const uint16_t* q, int64_t q_stride, const trellis_kv_cache* cache,
+                           const trellis_kv_state* state, const int32_t* seq_ids, int n, const int32_t* q_start,
+                           const int64_t* ancestors, int64_t tokens, int heads_q, int max_q, float scale,
+                           uint16_t* out, void* workspace, size_t workspace_bytes, void* stream);
+size_t trellis_window_attention_workspace_bytes(const trellis_kv_cache* cache, const trellis_kv_state* state, int n,
+                                                int64_t tokens, int heads_q, int max_q, int window, int sinks);
+int trellis_window_attention(const uint16_t* q, int64_t q_stride, const trellis_kv_cache* cache,
+                             const trellis_kv_state* state, const int32_t* seq_ids, int n, const int32_t* q_start,
+                             int64_t tokens, int heads_q, int max_q, int window, int sinks, float scale,
+                             uint16_t* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * trellis_cache_reserve -- storage for new tokens.  Entry b (of n,
+ * 1..TRELLIS_CACHE_MAX_SEQS) wants q_start[b+1] - q_start[b] tokens behind the
+ * lengths of sequence seq_ids[b]; pages that it does not hold yet are taken
+ * from the free ones, lowest number first, in list order.  granted[b] = 1 if
+ * the entry has all its pages, else 0 and nothing of it changed: the tokens
+ * pass the table's width, a repeated or unknown sequence, or the free pages do
+ * not reach for it and the entries before it (refused ones included).
+ *   slots int32 [tokens]: the slot of every token, -1 where refused
+ * lengths is not changed (trellis_cache_accept does that).
+ *
+ * trellis_cache_fork -- child children[b] becomes what parents[b] was before
+ * the call: full pages are shared (refs + 1), the last partial page is copied
+ * into a free one (lowest first, list order) in every layer, lengths is copied.
+ * The child's earlier pages are returned first, so children may be reused, and
+ * parents replaced in the same call (beam search).  granted[b] = 0: no free
+ * page, an unknown parent or a parent without the pages of its length (the
+ * child is left empty), a repeated or unknown child (nothing done).  A child
+ * that is its own parent is left as it is.
+ *
+ * trellis_cache_accept -- the kept rows of a drafted tree move up behind the
+ * cached tokens: in every layer row lengths + j becomes what row
+ * lengths + path[b][j] was before the call, j < counts[b], and new_lengths =
+ * lengths + counts for the listed sequences (unchanged for the others;
+ * new_lengths may be lengths itself).  path int32 [n, max_path], max_path
+ * 1..TRELLIS_ACCEPT_MAX, ascending with path[j] >= j; counts int32 [n].  After a
+ * chain that is kept whole, path = 0, 1, 2, ...  For a prompt that is longer
+ * than max_path, add to lengths instead.  Rows without storage stay, repeated
+ * sequences count once.
+ *
+ * trellis_cache_free -- the pages of the listed sequences are returned
+ * (refs - 1), their table rows become -1, their lengths 0.
+ */
+size_t trellis_cache_reserve_workspace_bytes(const trellis_kv_cache* cache, const trellis_kv_state* state, int n);
+int trellis_cache_reserve(const trellis_kv_cache* cache, const trellis_kv_state* state, const int32_t* seq_ids, int n,
+                          const int32_t* q_start, int64_t tokens, int32_t* slots, int32_t* granted, void* workspace,
+                          size_t workspace_bytes, void* stream);
+size_t trellis_cache_fork_workspace_bytes(const trellis_kv_cache* cache, const trellis_kv_state* state, int n);
+int trellis_cache_fork(const trellis_kv_cache* cache, const trellis_kv_state* state, const int32_t* parents,
+                       const int32_t* children, int n, int32_t* granted, void* workspace, size_t workspace_bytes,
+                       void* stream);
+int trellis_cache_accept(const trellis_kv_cache* cache, const trellis_kv_state* state, const int32_t* seq_ids, int n,
+                         const int32_t* path, int max_path, const int32_t* counts, int32_t* new_lengths, void* stream);
+int trellis_cache_free(const trellis_kv_cache* cache, const trellis_kv_state* state, const int32_t* seq_ids, int n,
+                       void* stream);
+
 /* Description of the last non-OK status on this thread ("" if none). */
 const char* trellis_last_error(void);
 

@@ -12,6 +12,12 @@ Tensor conventions (all CUDA/HIP device tensors, contiguous):
   codes  int32/uint32 [rows, cols*k/32]  packed code words
   scales float16 [rows]
   x      bfloat16 [M, in_features]
+
+Attention between the projections (one paged key/value cache):
+  k_cache  bfloat16/float16 [(layers,) pages, kv_heads, D/8, P, 8]
+  v_cache  the same type    [(layers,) pages, kv_heads, P/8, D, 8]
+  table    int32 [seqs, width] page numbers, -1: none
+  lengths  int32 [seqs] cached tokens;  refs  int32 [pages] holders of a page
 """
 import ctypes
 import os
@@ -26,6 +32,10 @@ OUT_BF16, OUT_F32 = 0, 1
 PREFILL_FUSED, PREFILL_EXPAND_GEMM, PREFILL_AUTO = 0, 1, 2
 MATVEC_MAX_M = 4
 GROUP_MAX = 4
+KV_BF16, KV_F16 = 0, 1
+TREE_MAX = 64
+ACCEPT_MAX = 64
+CACHE_MAX_SEQS = 1024
 
 # every symbol include/trellis.h declares
 EXPORTS = (
@@ -38,6 +48,11 @@ EXPORTS = (
     "trellis_prefill_axis0_workspace_bytes", "trellis_prefill_axis0", "trellis_prefill_axis0_il",
     "trellis_prefill_tune", "trellis_prefill_axis0_tune",
     "trellis_probe_decode_only", "trellis_probe_gateup_decode_free",
+    "trellis_qk_norm_rope",
+    "trellis_tree_attention_workspace_bytes", "trellis_tree_attention",
+    "trellis_window_attention_workspace_bytes", "trellis_window_attention",
+    "trellis_cache_reserve_workspace_bytes", "trellis_cache_reserve",
+    "trellis_cache_fork_workspace_bytes", "trellis_cache_fork", "trellis_cache_accept", "trellis_cache_free",
     "trellis_decode_states", "trellis_last_error", "trellis_version",
 )
 
@@ -46,6 +61,19 @@ class TrellisError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"[status {status}] {msg}")
         self.status = status
+
+
+class KvCache(ctypes.Structure):
+    """trellis_kv_cache of include/trellis.h"""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", ctypes.c_int64), ("layers", ctypes.c_int),
+                ("heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("dtype", ctypes.c_int)]
+
+
+class KvState(ctypes.Structure):
+    """trellis_kv_state of include/trellis.h"""
+    _fields_ = [("table", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("seqs", ctypes.c_int64), ("width", ctypes.c_int64)]
 
 
 _lib = None
@@ -96,6 +124,20 @@ def load_library():
         "trellis_probe_gateup_decode_free": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _int, _int, _int,
                                                     _int, _vp]),
         "trellis_decode_states": (_int, [_vp, _i64, _i64, _int, _int, _int, _vp, _vp, _vp, _vp]),
+        "trellis_qk_norm_rope": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _int, _int,
+                                        ctypes.c_float, _vp, _vp, _vp, _i64, _int, _vp]),
+        "trellis_tree_attention_workspace_bytes": (_sz, [_vp, _vp, _int, _i64, _int, _int]),
+        "trellis_tree_attention": (_int, [_vp, _i64, _vp, _vp, _vp, _int, _vp, _vp, _i64, _int, _int,
+                                          ctypes.c_float, _vp, _vp, _sz, _vp]),
+        "trellis_window_attention_workspace_bytes": (_sz, [_vp, _vp, _int, _i64, _int, _int, _int, _int]),
+        "trellis_window_attention": (_int, [_vp, _i64, _vp, _vp, _vp, _int, _vp, _i64, _int, _int, _int, _int,
+                                            ctypes.c_float, _vp, _vp, _sz, _vp]),
+        "trellis_cache_reserve_workspace_bytes": (_sz, [_vp, _vp, _int]),
+        "trellis_cache_reserve": (_int, [_vp, _vp, _vp, _int, _vp, _i64, _vp, _vp, _vp, _sz, _vp]),
+        "trellis_cache_fork_workspace_bytes": (_sz, [_vp, _vp, _int]),
+        "trellis_cache_fork": (_int, [_vp, _vp, _vp, _vp, _int, _vp, _vp, _sz, _vp]),
+        "trellis_cache_accept": (_int, [_vp, _vp, _vp, _int, _vp, _int, _vp, _vp, _vp]),
+        "trellis_cache_free": (_int, [_vp, _vp, _vp, _int, _vp]),
         "trellis_last_error": (ctypes.c_char_p, []),
         "trellis_version": (ctypes.c_char_p, []),
     }
@@ -450,3 +492,233 @@ def probe_gateup_decode_free(gcodes, gscales, ucodes, uscales, x, k, L=12, T=256
     _check(load_library().trellis_probe_gateup_decode_free(_ptr(gcodes), _ptr(gscales), _ptr(ucodes), _ptr(uscales),
                                                            _ptr(x), _ptr(out), R, C, M, k, L, T, _stream(x.device)))
     return out
+
+
+# ---- attention between the projections ------------------------------------
+
+_KV = {torch.bfloat16: KV_BF16, torch.float16: KV_F16}
+
+
+def _kv_cache(k_cache, v_cache, layered):
+    """KvCache of the two pools after checking that they are one cache."""
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not layered and t.dim() != 5:
+            raise ValueError(f"{name}: expected one layer [pages, heads, ., ., 8], got shape {tuple(t.shape)}")
+        _need(t, name, tuple(_KV), 6 if layered and t.dim() == 6 else 5)
+    layers = k_cache.shape[0] if k_cache.dim() == 6 else 1
+    pages, heads, blocks, page_size, eight = k_cache.shape[-5:]
+    want = tuple(k_cache.shape[:-5]) + (pages, heads, page_size // 8, blocks * 8, 8)
+    if eight != 8 or tuple(v_cache.shape) != want:
+        raise ValueError(f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} are not one cache: keys "
+                         f"[pages, heads, D/8, P, 8], values [pages, heads, P/8, D, 8]")
+    if v_cache.dtype != k_cache.dtype or v_cache.device != k_cache.device:
+        raise ValueError("k_cache and v_cache differ in dtype or device")
+    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), pages, layers, heads, blocks * 8, page_size,
+                   _KV[k_cache.dtype])
+
+
+def _i32(t, name, shape, device):
+    """A device tensor of 32-bit whole numbers of that shape (None: any size)."""
+    _need(t, name, (torch.int32,), len(shape))
+    if any(w is not None and w != g for w, g in zip(shape, t.shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call on {device}")
+    return t
+
+
+def _kv_state(table, lengths, refs, pages, device):
+    _i32(table, "table", (None, None), device)
+    _i32(lengths, "lengths", (table.shape[0],), device)
+    if refs is not None:
+        _i32(refs, "refs", (pages,), device)
+    return KvState(table.data_ptr(), lengths.data_ptr(), None if refs is None else refs.data_ptr(), table.shape[0],
+                   table.shape[1])
+
+
+def _head_rows(t, name, heads, head_dim, dtype, device):
+    """[tokens, heads, D] whose rows may be a view of a wider tensor; its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, the cache holds {dtype}")
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != head_dim:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [tokens, {heads or 'heads'}, {head_dim}]")
+    if t.device != device or t.device.type != "cuda":
+        raise ValueError(f"{name} must be a device tensor on {device}")
+    row = t.shape[1] * head_dim
+    if t.shape[0] < 1 or t.shape[1] < 1:
+        return row
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != head_dim):
+        raise ValueError(f"{name}: the heads of a row must be contiguous, got strides {t.stride()}")
+    return t.stride(0) if t.shape[0] > 1 else row
+
+
+def qk_norm_rope(q, k, v, q_weight, k_weight, positions, inv_freq, slots, k_cache, v_cache, eps=1e-6,
+                 interleaved=False, out=None):
+    """RMS norm of every head of q [N, Hq, D] and k [N, Hkv, D], rotation of the
+    first 2 * len(inv_freq) dimensions by positions * inv_freq, and the append
+    of k and v to the cache at `slots` (int32 [N], -1: not cached).  q, k and v
+    may be views of one projection output.  Returns the queries [N, Hq, D]."""
+    cache = _kv_cache(k_cache, v_cache, False)
+    dev, D, dt = k_cache.device, cache.head_dim, k_cache.dtype
+    qs = _head_rows(q, "q", None, D, dt, dev)
+    ks = _head_rows(k, "k", cache.heads, D, dt, dev)
+    vs = _head_rows(v, "v", cache.heads, D, dt, dev)
+    N = q.shape[0]
+    if k.shape[0] != N or v.shape[0] != N:
+        raise ValueError(f"q, k and v have {N}, {k.shape[0]} and {v.shape[0]} tokens")
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        _need(t, name, (dt,), 1)
+        if t.numel() != D:
+            raise ValueError(f"{name} has {t.numel()} entries, a head has {D}")
+    _need(inv_freq, "inv_freq", (torch.float32,), 1)
+    _i32(positions, "positions", (N,), dev)
+    _i32(slots, "slots", (N,), dev)
+    out = _out(out, "out", (N, q.shape[1], D), (dt,), dev)
+    with torch.cuda.device(dev):
+        _check(load_library().trellis_qk_norm_rope(
+            _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq),
+            2 * inv_freq.numel(), int(interleaved), eps, _ptr(slots), _ptr(out), ctypes.byref(cache), N, q.shape[1],
+            _stream(dev)))
+    return out
+
+
+def _attention(q, k_cache, v_cache, table, lengths, q_start, max_q, scale, seq_ids, out):
+    """what the two attention calls share: (cache, state, entries, row stride, scale, out)"""
+    cache = _kv_cache(k_cache, v_cache, False)
+    dev = k_cache.device
+    stride = _head_rows(q, "q", None, cache.head_dim, k_cache.dtype, dev)
+    state = _kv_state(table, lengths, None, cache.pages, dev)
+    _i32(q_start, "q_start", (None,), dev)
+    n = q_start.numel() - 1
+    if seq_ids is not None:
+        _i32(seq_ids, "seq_ids", (n,), dev)
+    elif n > table.shape[0]:
+        raise ValueError(f"q_start has {n} entries, the table {table.shape[0]} sequences")
+    out = _out(out, "out", tuple(q.shape), (k_cache.dtype,), dev)
+    return cache, state, n, stride, cache.head_dim ** -0.5 if scale is None else scale, out
+
+
+def tree_attention(q, k_cache, v_cache, table, lengths, q_start, ancestors, max_q, scale=None, seq_ids=None, out=None,
+                   workspace=None):
+    """Attention of drafted tokens over the cache and their ancestors.  q [N, Hq,
+    D]; entry e is sequence e (or seq_ids[e]) with rows q_start[e] ..
+    q_start[e+1]-1, at most max_q (<= 64) of them, cached behind `lengths`.
+    ancestors int64 [N]: bit m set if the row sees the entry's token m.  scale
+    defaults to D ** -0.5.  Returns [N, Hq, D]."""
+    cache, state, n, stride, scale, out = _attention(q, k_cache, v_cache, table, lengths, q_start, max_q, scale,
+                                                     seq_ids, out)
+    _need(ancestors, "ancestors", (torch.int64,), 1)
+    if ancestors.numel() != q.shape[0] or ancestors.device != q.device:
+        raise ValueError(f"ancestors has {ancestors.numel()} entries on {ancestors.device}, q {q.shape[0]} rows")
+    lib, c, s = load_library(), ctypes.byref(cache), ctypes.byref(state)
+    with torch.cuda.device(q.device):
+        need = lib.trellis_tree_attention_workspace_bytes(c, s, n, q.shape[0], q.shape[1], max_q)
+        ws, wsb = _workspace(need, q.device, workspace)
+        _check(lib.trellis_tree_attention(_ptr(q), stride, c, s, _ptr(seq_ids), n, _ptr(q_start), _ptr(ancestors),
+                                          q.shape[0], q.shape[1], max_q, scale, _ptr(out), _ptr(ws), wsb,
+                                          _stream(q.device)))
+    return out
+
+
+def window_attention(q, k_cache, v_cache, table, lengths, q_start, max_q, window=0, sinks=0, scale=None, seq_ids=None,
+                     out=None, workspace=None):
+    """Causal attention of new tokens over the cache: the token at position p
+    sees the keys j <= p with p - j < window (0: no limit) or j < sinks.
+    Arguments otherwise as tree_attention; max_q has no upper bound."""
+    cache, state, n, stride, scale, out = _attention(q, k_cache, v_cache, table, lengths, q_start, max_q, scale,
+                                                     seq_ids, out)
+    lib, c, s = load_library(), ctypes.byref(cache), ctypes.byref(state)
+    with torch.cuda.device(q.device):
+        need = lib.trellis_window_attention_workspace_bytes(c, s, n, q.shape[0], q.shape[1], max_q, window, sinks)
+        ws, wsb = _workspace(need, q.device, workspace)
+        _check(lib.trellis_window_attention(_ptr(q), stride, c, s, _ptr(seq_ids), n, _ptr(q_start), q.shape[0],
+                                            q.shape[1], max_q, window, sinks, scale, _ptr(out), _ptr(ws), wsb,
+                                            _stream(q.device)))
+    return out
+
+
+def kv_cache(layers, pages, heads, head_dim, page_size, dtype=torch.bfloat16, device="cuda"):
+    """Empty pools (k_cache, v_cache) of `layers` layers; k_cache[i], v_cache[i] are one layer."""
+    k = torch.zeros((layers, pages, heads, head_dim // 8, page_size, 8), dtype=dtype, device=device)
+    return k, torch.zeros((layers, pages, heads, page_size // 8, head_dim, 8), dtype=dtype, device=device)
+
+
+def kv_state(seqs, width, pages, device="cuda"):
+    """Empty (table, lengths, refs): `seqs` sequences of at most `width` pages."""
+    return (torch.full((seqs, width), -1, dtype=torch.int32, device=device),
+            torch.zeros(seqs, dtype=torch.int32, device=device), torch.zeros(pages, dtype=torch.int32, device=device))
+
+
+def cache_reserve(table, lengths, refs, page_size, seq_ids, q_start, tokens, slots=None, granted=None, workspace=None):
+    """Slots for new tokens: entry b wants q_start[b+1] - q_start[b] tokens behind
+    sequence seq_ids[b]; `tokens` in all.  Missing pages are taken from the free
+    ones, lowest first.  Returns (slots int32 [tokens], -1 where refused,
+    granted int32 [n])."""
+    _need(refs, "refs", (torch.int32,), 1)
+    dev, pages = refs.device, refs.numel()
+    state = _kv_state(table, lengths, refs, pages, dev)
+    cache = KvCache(None, None, pages, 1, 1, 64, page_size, KV_BF16)
+    _i32(seq_ids, "seq_ids", (None,), dev)
+    n = seq_ids.numel()
+    _i32(q_start, "q_start", (n + 1,), dev)
+    slots = _out(slots, "slots", (tokens,), (torch.int32,), dev)
+    granted = _out(granted, "granted", (n,), (torch.int32,), dev)
+    lib, c, s = load_library(), ctypes.byref(cache), ctypes.byref(state)
+    with torch.cuda.device(dev):
+        ws, wsb = _workspace(lib.trellis_cache_reserve_workspace_bytes(c, s, n), dev, workspace)
+        _check(lib.trellis_cache_reserve(c, s, _ptr(seq_ids), n, _ptr(q_start), tokens, _ptr(slots), _ptr(granted),
+                                         _ptr(ws), wsb, _stream(dev)))
+    return slots, granted
+
+
+def cache_fork(k_cache, v_cache, table, lengths, refs, parents, children, granted=None, workspace=None):
+    """children[b] becomes a copy of parents[b]: full pages shared, the last
+    partial page copied in every layer.  Returns granted int32 [n]."""
+    cache = _kv_cache(k_cache, v_cache, True)
+    dev = k_cache.device
+    state = _kv_state(table, lengths, refs, cache.pages, dev)
+    _i32(parents, "parents", (None,), dev)
+    n = parents.numel()
+    _i32(children, "children", (n,), dev)
+    granted = _out(granted, "granted", (n,), (torch.int32,), dev)
+    lib, c, s = load_library(), ctypes.byref(cache), ctypes.byref(state)
+    with torch.cuda.device(dev):
+        ws, wsb = _workspace(lib.trellis_cache_fork_workspace_bytes(c, s, n), dev, workspace)
+        _check(lib.trellis_cache_fork(c, s, _ptr(parents), _ptr(children), n, _ptr(granted), _ptr(ws), wsb,
+                                      _stream(dev)))
+    return granted
+
+
+def cache_accept(k_cache, v_cache, table, lengths, seq_ids, path, counts, new_lengths=None):
+    """Drafted rows path[b][: counts[b]] of sequence seq_ids[b] move up behind its
+    cached tokens in every layer; lengths grows by counts (in place, or into
+    new_lengths).  Returns the new lengths."""
+    cache = _kv_cache(k_cache, v_cache, True)
+    dev = k_cache.device
+    state = _kv_state(table, lengths, None, cache.pages, dev)
+    _i32(seq_ids, "seq_ids", (None,), dev)
+    n = seq_ids.numel()
+    _i32(path, "path", (n, None), dev)
+    _i32(counts, "counts", (n,), dev)
+    new_lengths = lengths if new_lengths is None else _i32(new_lengths, "new_lengths", (table.shape[0],), dev)
+    with torch.cuda.device(dev):
+        _check(load_library().trellis_cache_accept(ctypes.byref(cache), ctypes.byref(state), _ptr(seq_ids), n,
+                                                   _ptr(path), path.shape[1], _ptr(counts), _ptr(new_lengths),
+                                                   _stream(dev)))
+    return new_lengths
+
+
+def cache_free(table, lengths, refs, seq_ids):
+    """The pages of the listed sequences are returned; their rows become empty."""
+    _need(refs, "refs", (torch.int32,), 1)
+    dev = refs.device
+    state = _kv_state(table, lengths, refs, refs.numel(), dev)
+    _i32(seq_ids, "seq_ids", (None,), dev)
+    cache = KvCache(None, None, refs.numel(), 1, 1, 64, 16, KV_BF16)
+    with torch.cuda.device(dev):
+        _check(load_library().trellis_cache_free(ctypes.byref(cache), ctypes.byref(state), _ptr(seq_ids),
+                                                 seq_ids.numel(), _stream(dev)))

@@ -104,6 +104,26 @@ int hip_status(const char* fn, hipError_t e) {
   return fail(TRELLIS_EHIP, "%s: HIP error %d (%s)", fn, (int)e, hipGetErrorString(e));
 }
 
+}  // namespace
+
+namespace trellis {
+
+int api_fail(int code, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof(g_err), fmt, ap);
+  va_end(ap);
+  return code;
+}
+
+int api_ok() { return ok(); }
+
+int api_hip(const char* fn, hipError_t e) { return hip_status(fn, e); }
+
+}  // namespace trellis
+
+namespace {
+
 #define TRY(expr)            \
   do {                       \
     int _rc = (expr);        \

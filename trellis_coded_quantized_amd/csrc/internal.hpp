@@ -75,4 +75,70 @@ hipError_t launch_prefill_fused(const uint32_t* codes, const uint16_t* scales, c
                                 uint16_t* out, int64_t R, int64_t C, int64_t M, int k,
                                 void* workspace, hipStream_t stream, int axis0 = 0, int interleave = 0);
 
+// ---- attention over the paged cache and its page operations --------------
+
+// Errors of the C entry points, wherever they are defined: set the thread's
+// message and return the status.
+int api_fail(int code, const char* fmt, ...);
+int api_ok();
+int api_hip(const char* fn, hipError_t e);
+
+// One attention call.  TREE: `ancestors` is set, window and sinks are 0.
+struct AttnArgs {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  const int32_t* table;       // [seqs, width] pages
+  const int32_t* lengths;     // [seqs]
+  const int32_t* seq_ids;     // [entries] or NULL: entry e is sequence e
+  const int32_t* q_start;     // [entries + 1]
+  const int64_t* ancestors;   // [tokens], tree only
+  uint16_t* out;
+  float* part_o;              // partial outputs of split entries
+  float* part_ml;             // their (bound, sum) pairs
+  int64_t tokens, q_stride, width, seqs;
+  uint32_t pages;
+  int entries, max_q, heads_q, heads_kv, head_dim, page_log2;
+  int window, sinks, fp16;
+  int target;                 // few-row kernel: workgroups wanted per key head
+  int splits;                 // many-row kernel: parts of every unit's keys
+  float scale;
+};
+
+// Workspace of a call: filled into the args' part_* by launch_attention.
+size_t attention_workspace_bytes(const AttnArgs& a);
+hipError_t launch_attention(AttnArgs a, void* workspace, hipStream_t stream);
+
+struct QkNormRopeArgs {
+  const uint16_t *q, *k, *v, *q_weight, *k_weight;
+  const int32_t *positions, *slots;
+  const float* inv_freq;
+  uint16_t *out, *k_cache, *v_cache;
+  int64_t q_stride, k_stride, v_stride, tokens;
+  uint32_t pages;
+  int heads_q, heads_kv, head_dim, rotary, page_log2, interleaved, fp16;
+  float eps;
+};
+hipError_t launch_qk_norm_rope(const QkNormRopeArgs& a, hipStream_t stream);
+
+// Page operations.  table / lengths / refs are the cache's device state.
+struct CacheArgs {
+  uint16_t *k, *v;            // [layers, pages, heads, ...]
+  int32_t *table, *lengths, *refs;
+  int64_t seqs, width;
+  uint32_t pages;
+  int layers, heads, head_dim, page_log2;
+};
+constexpr int kCacheMaxEntries = 1024;    // sequences in one page operation
+constexpr int kCacheMaxPath = 64;         // drafted rows kept by one accept
+hipError_t launch_cache_reserve(const CacheArgs& c, const int32_t* seq_ids, int n, const int32_t* q_start,
+                                int64_t tokens, int32_t* slots, int32_t* granted, void* workspace, hipStream_t stream);
+size_t cache_reserve_workspace_bytes(const CacheArgs& c, int n);
+hipError_t launch_cache_fork(const CacheArgs& c, const int32_t* parents, const int32_t* children, int n,
+                             int32_t* granted, void* workspace, hipStream_t stream);
+size_t cache_fork_workspace_bytes(const CacheArgs& c, int n);
+hipError_t launch_cache_accept(const CacheArgs& c, const int32_t* seq_ids, int n, const int32_t* path, int max_path,
+                               const int32_t* counts, int32_t* new_lengths, hipStream_t stream);
+hipError_t launch_cache_free(const CacheArgs& c, const int32_t* seq_ids, int n, hipStream_t stream);
+
 }  // namespace trellis
