@@ -135,27 +135,20 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_few_kern
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[d][r] *= alpha;
     }
-    u32x4v p[2];
-    pack_weights<T>(sc[0], p);
-    if (open) {
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) o[d] = T::mfma(vf[s][d], p[s], o[d]);
-    } else {
-      u32x4v seen[2];
+    bool bad = false;
+    if (!open) {
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const int key = kb + s * 16 + half * 8 + 2 * w;
-          seen[s][w] = (mask.sees<TREE>(key) ? T::kOne : 0u) | (mask.sees<TREE>(key + 1) ? T::kOne << 16 : 0u);
-        }
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) o[d] = mfma_masked<T>(vf[s][d], p[s], seen[s], o[d]);
+        for (int d = 0; d < DT; ++d) bad |= drop_nonfinite<T>(vf[s][d]);
     }
+    u32x4v p[2];
+    pack_weights<T>(sc[0], p);
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) o[d] = T::mfma(vf[s][d], p[s], o[d]);
+    if (__any(bad)) add_nonfinite<T, D, TREE>(a, e, mask, h, kb, 32, o);
   }
 
   // join the four waves
@@ -217,6 +210,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_many_ker
   constexpr int GRAN = KT * D / 8;                           // granules of one operand's tile
   constexpr int PER = GRAN / kThreads;
   extern __shared__ __align__(16) u32x4v lds[];              // [2][keys, values][GRAN]
+  __shared__ int s_bad[2];
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, col = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int split = blockIdx.x % a.splits, rt = gridDim.x / a.splits - 1 - blockIdx.x / a.splits;
@@ -248,26 +242,38 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_many_ker
   const float c = a.scale * kLog2e;
 
   u32x4v kin[PER], vin[PER];
+  // The page of each of a tile's keys, one key a lane.
+  auto pages_of = [&](int t) {
+    const int key = list.key<KT>(min(t, t1 - 1)) + lane;
+    return e.pages[min(key >> a.page_log2, (int)a.width - 1)];
+  };
   // keys: granule g of the tile is dimension block g / 64 of key g % 64, so
   // a thread keeps its key; values: granule g is token block g / D of
-  // dimension g % D.
-  auto fetch = [&](int t) {
+  // dimension g % D, one token block a wave.
+  auto fetch = [&](int t, int32_t pk) {
     const int kb = list.key<KT>(t);
-    const int key = kb + lane;
-    const int32_t pk = e.pages[min(key >> a.page_log2, (int)a.width - 1)];
-    const uint16_t* kp = a.k + ((int64_t)page_in_pool(pk, a.pages) * a.heads_kv + h) * head_elems + (key & pmask) * 8;
+    const uint16_t* kp = a.k + ((int64_t)page_in_pool(pk, a.pages) * a.heads_kv + h) * head_elems +
+                         ((kb + lane) & pmask) * 8 + (int64_t)wave * P * 8;
 #pragma unroll
-    for (int n = 0; n < PER; ++n) kin[n] = *reinterpret_cast<const u32x4v*>(kp + (int64_t)(n * kWaves + wave) * P * 8);
+    for (int n = 0; n < PER; ++n) kin[n] = *reinterpret_cast<const u32x4v*>(kp + (int64_t)n * kWaves * P * 8);
 #pragma unroll
     for (int n = 0; n < PER; ++n) {
-      const int g = n * kThreads + tid, tg = g / D, d = g % D, first = kb + tg * 8;
-      const int32_t pv = e.pages[min(first >> a.page_log2, (int)a.width - 1)];
-      vin[n] = *reinterpret_cast<const u32x4v*>(a.v + ((int64_t)page_in_pool(pv, a.pages) * a.heads_kv + h) * head_elems +
-                                                (int64_t)((first & pmask) >> 3) * D * 8 + d * 8);
+      const int g = n * kThreads + wave * 64, tg = g / D, first = kb + tg * 8;
+      const int32_t pv = __builtin_amdgcn_readlane(pk, tg * 8);
+      const uint16_t* vp = a.v + ((int64_t)page_in_pool(pv, a.pages) * a.heads_kv + h) * head_elems +
+                           (int64_t)((first & pmask) >> 3) * D * 8 + (g % D) * 8;
+      vin[n] = *reinterpret_cast<const u32x4v*>(vp + lane * 8);
     }
   };
-  auto store = [&](int buf) {
+  // s_bad: the last tile whose values had to be cleaned
+  auto store = [&](int buf, int t) {
     u32x4v* dst = lds + buf * 2 * GRAN;
+    if (!tile_open<KT, TREE>(a, e, i0, i1, list.key<KT>(t))) {
+      bool bad = false;
+#pragma unroll
+      for (int n = 0; n < PER; ++n) bad |= drop_nonfinite<T>(vin[n]);
+      if (bad) s_bad[buf] = t;
+    }
 #pragma unroll
     for (int n = 0; n < PER; ++n) {
       dst[n * kThreads + tid] = kin[n];
@@ -275,9 +281,13 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_many_ker
     }
   };
 
+  if (tid < 2) s_bad[tid] = -1;
+  lds_barrier();
+  int32_t next = 0;
   if (t0 < t1) {
-    fetch(t0);
-    store(0);
+    fetch(t0, pages_of(t0));
+    next = pages_of(t0 + 1);
+    store(0, t0);
   }
   lds_barrier();
   const int krow = tile_key_of_row(col);
@@ -285,14 +295,16 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_many_ker
     const int buf = (t - t0) & 1, kb = list.key<KT>(t);
     const u32x4v* kt = lds + buf * 2 * GRAN;
     const u32x4v* vt = kt + GRAN;
-    if (t + 1 < t1) fetch(t + 1);
+    if (t + 1 < t1) {
+      fetch(t + 1, next);
+      next = pages_of(t + 2);
+    }
     f32x16 sc[2] = {f32x16{}, f32x16{}};
 #pragma unroll
     for (int s = 0; s < STEPS; ++s)
 #pragma unroll
       for (int x = 0; x < 2; ++x) sc[x] = T::mfma(kt[(2 * s + half) * KT + x * 32 + krow], q[s], sc[x]);
-    const bool open = tile_open<KT, TREE>(a, e, i0, i1, kb);
-    if (!open) {
+    if (!tile_open<KT, TREE>(a, e, i0, i1, kb)) {
 #pragma unroll
       for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -312,27 +324,13 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_many_ker
     for (int x = 0; x < 2; ++x) {
       u32x4v p[2];
       pack_weights<T>(sc[x], p);
-      if (open) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+      for (int s = 0; s < 2; ++s)
 #pragma unroll
-          for (int d = 0; d < DT; ++d) o[d] = T::mfma(vt[(x * 4 + 2 * s + half) * D + d * 32 + col], p[s], o[d]);
-      } else {
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          u32x4v seen;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const int key = kb + x * 32 + s * 16 + half * 8 + 2 * w;
-            seen[w] = (mask.sees<TREE>(key) ? T::kOne : 0u) | (mask.sees<TREE>(key + 1) ? T::kOne << 16 : 0u);
-          }
-#pragma unroll
-          for (int d = 0; d < DT; ++d)
-            o[d] = mfma_masked<T>(vt[(x * 4 + 2 * s + half) * D + d * 32 + col], p[s], seen, o[d]);
-        }
-      }
+        for (int d = 0; d < DT; ++d) o[d] = T::mfma(vt[(x * 4 + 2 * s + half) * D + d * 32 + col], p[s], o[d]);
     }
-    if (t + 1 < t1) store(buf ^ 1);
+    if (s_bad[buf] == t) add_nonfinite<T, D, TREE>(a, e, mask, h, kb, KT, o);
+    if (t + 1 < t1) store(buf ^ 1, t + 1);
     lds_barrier();
   }
 

@@ -136,16 +136,6 @@ __device__ __forceinline__ bool tile_open(const AttnArgs& a, const Entry& e, int
   return a.window <= 0 || kb >= e.ctx + i1 - a.window + 1 || kb + KT <= a.sinks;
 }
 
-// Whether a value operand holds an infinity or NaN.
-template <typename T>
-__device__ __forceinline__ bool has_nonfinite(u32x4v v) {
-  bool any = false;
-#pragma unroll
-  for (int w = 0; w < 4; ++w)
-    any |= (v[w] & T::kExp) == T::kExp || (v[w] & (T::kExp << 16)) == (T::kExp << 16);
-  return any;
-}
-
 // The running softmax of the rows a wave owns.
 struct Running {
   float m;     // bound on c * score (-inf: no visible key yet), equal in both lane halves
@@ -194,41 +184,42 @@ __device__ __forceinline__ void pack_weights(const f32x16& s, u32x4v (&p)[2]) {
     for (int w = 0; w < 4; ++w) p[h][w] = T::pack(s[8 * h + 2 * w], s[8 * h + 2 * w + 1]);
 }
 
-// O^T += V^T P^T for one value operand of a tile in which some rows see some
-// keys only.  Zero weights do not hide an infinity or NaN in the values
-// (0 * inf = NaN), and such values may stand where nothing was ever
-// written, so they enter the product as zeros, and rows that do see one get
-// it back: products of indicators count, per row and dimension, the visible
-// +inf, -inf and NaN.  `seen`: the operand of ones where the row sees the key.
+// Zero weights do not hide an infinity or NaN among the values (0 * inf =
+// NaN), and such values may stand where a row does not look, or where nothing
+// was ever written.  In a tile that some row sees in part they therefore
+// enter the product as zeros (drop_nonfinite, which says whether there were
+// any), and rows that do see one get it back from here: each lane walks the
+// tile's keys and adds what its row sees to its own outputs.
 template <typename T>
-__device__ __forceinline__ f32x16 mfma_masked(u32x4v v, u32x4v p, u32x4v seen, f32x16 acc) {
-  if (!__any(has_nonfinite<T>(v))) return T::mfma(v, p, acc);
-  u32x4v clean = v, kinds[3];
+__device__ __forceinline__ bool drop_nonfinite(u32x4v& v) {
+  bool any = false;
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
-    kinds[0][w] = kinds[1][w] = kinds[2][w] = 0;
-#pragma unroll
-    for (int h = 0; h < 32; h += 16) {
-      const uint32_t x = (v[w] >> h) & 0xFFFFu;
-      if ((x & T::kExp) != T::kExp) continue;
-      clean[w] &= ~(0xFFFFu << h);
-      const int kind = x == T::kExp ? 0 : x == (T::kExp | 0x8000u) ? 1 : 2;
-      if (kind == 0) kinds[0][w] |= T::kOne << h;
-      else if (kind == 1) kinds[1][w] |= T::kOne << h;
-      else kinds[2][w] |= T::kOne << h;
-    }
+    const uint32_t x = v[w];
+    const bool lo = (x & T::kExp) == T::kExp, hi = (x & (T::kExp << 16)) == (T::kExp << 16);
+    v[w] = (lo ? 0u : x & 0xFFFFu) | (hi ? 0u : x & 0xFFFF0000u);
+    any |= lo || hi;
   }
-  acc = T::mfma(clean, p, acc);
-  const f32x16 zero = {};
+  return any;
+}
+
+template <typename T, int D, bool TREE>
+__device__ __forceinline__ void add_nonfinite(const AttnArgs& a, const Entry& e, const RowMask& mask, int h, int kb,
+                                              int keys, f32x16 (&o)[D / 32]) {
+  const int half = (int)__lane_id() >> 5, P = 1 << a.page_log2;
+  for (int key = kb; key < kb + keys; ++key) {
+    if (!mask.sees<TREE>(key)) continue;
+    const uint16_t* v = a.v + ((int64_t)page_in_pool(e.pages[key >> a.page_log2], a.pages) * a.heads_kv + h) *
+                                  ((int64_t)D << a.page_log2) +
+                        (int64_t)((key & (P - 1)) >> 3) * D * 8 + (key & 7);
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    const f32x16 hits = T::mfma(kinds[k], seen, zero);
-    const float put = k == 0 ? INFINITY : k == 1 ? -INFINITY : NAN;
+    for (int d = 0; d < D / 32; ++d)
 #pragma unroll
-    for (int r = 0; r < 16; ++r)
-      if (hits[r] > 0.0f) acc[r] += put;
+      for (int r = 0; r < 16; ++r) {
+        const uint16_t x = v[(d * 32 + 8 * (r >> 2) + 4 * half + (r & 3)) * 8];
+        if ((x & T::kExp) == T::kExp) o[d][r] += T::to_f32(x);
+      }
   }
-  return acc;
 }
 
 }  // namespace trellis
