@@ -495,65 +495,120 @@ def probe_gateup_decode_free(gcodes, gscales, ucodes, uscales, x, k, L=12, T=256
 
 
 # ---- attention between the projections ------------------------------------
+# These calls run many times a decode step on little data, so their checks are
+# kept to one pass of plain comparisons per tensor, and pointers go to the
+# library as integers.
 
 _KV = {torch.bfloat16: KV_BF16, torch.float16: KV_F16}
+_byref = ctypes.byref
+
+
+def _tensor(t, name, dtype, shape, index):
+    """Check a contiguous device tensor (shape entries of None: any size); its address."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    got = t.shape
+    if got != shape and (len(got) != len(shape) or any(w is not None and w != g for w, g in zip(shape, got))):
+        raise ValueError(f"{name}: shape {tuple(got)} of {t.numel()} entries, expected "
+                         f"{tuple('any' if w is None else w for w in shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be a device tensor on the device of the call, is on {t.device}")
+    return t.data_ptr()
+
+
+def _index(t, name):
+    """Device number of the tensor that a call runs by."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    return t.get_device()
+
+
+def _result(t, name, shape, dtype, device, index):
+    """A caller's output buffer or a new one, and its address."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    return t, _tensor(t, name, dtype, shape, index)
+
+
+def _scratch(nbytes, device, workspace):
+    """(tensor to keep alive, address, bytes) of a call's workspace."""
+    if nbytes == 0:
+        return None, None, 0
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), nbytes
+    if not (isinstance(workspace, torch.Tensor) and workspace.device == device and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous device tensor on the device of the call")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _call(fn, index, *args):
+    """fn(*args, current stream) with the device of the call current."""
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch.cuda.current_device() == index:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status != OK:
+        _check(status)
 
 
 def _kv_cache(k_cache, v_cache, layered):
-    """KvCache of the two pools after checking that they are one cache."""
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if not layered and t.dim() != 5:
-            raise ValueError(f"{name}: expected one layer [pages, heads, ., ., 8], got shape {tuple(t.shape)}")
-        _need(t, name, tuple(_KV), 6 if layered and t.dim() == 6 else 5)
-    layers = k_cache.shape[0] if k_cache.dim() == 6 else 1
-    pages, heads, blocks, page_size, eight = k_cache.shape[-5:]
-    want = tuple(k_cache.shape[:-5]) + (pages, heads, page_size // 8, blocks * 8, 8)
-    if eight != 8 or tuple(v_cache.shape) != want:
-        raise ValueError(f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} are not one cache: keys "
-                         f"[pages, heads, D/8, P, 8], values [pages, heads, P/8, D, 8]")
-    if v_cache.dtype != k_cache.dtype or v_cache.device != k_cache.device:
-        raise ValueError("k_cache and v_cache differ in dtype or device")
-    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), pages, layers, heads, blocks * 8, page_size,
-                   _KV[k_cache.dtype])
+    """(KvCache of the two pools after checking that they are one cache, device number)."""
+    index = _index(k_cache, "k_cache")
+    shape, dtype = k_cache.shape, k_cache.dtype
+    if dtype not in _KV:
+        raise TypeError(f"k_cache: dtype {dtype} not in {tuple(_KV)}")
+    n = len(shape)
+    if n != 5 and not (layered and n == 6):
+        raise ValueError(f"k_cache: expected {'[layers, ' if layered else 'one layer ['}pages, heads, D/8, P, 8], got "
+                         f"shape {tuple(shape)}")
+    if n == 6:
+        layers, pages, heads, blocks, page_size, eight = shape
+        want = (layers, pages, heads, page_size // 8, blocks * 8, 8)
+    else:
+        layers = 1
+        pages, heads, blocks, page_size, eight = shape
+        want = (pages, heads, page_size // 8, blocks * 8, 8)
+    if not isinstance(v_cache, torch.Tensor) or eight != 8 or v_cache.shape != want:
+        raise ValueError(f"k_cache {tuple(shape)} and v_cache {tuple(getattr(v_cache, 'shape', ()))} are not one "
+                         f"cache: keys [pages, heads, D/8, P, 8], values [pages, heads, P/8, D, 8]")
+    k = _tensor(k_cache, "k_cache", dtype, shape, index)
+    return KvCache(k, _tensor(v_cache, "v_cache", dtype, want, index), pages, layers, heads, blocks * 8, page_size,
+                   _KV[dtype]), index
 
 
-def _i32(t, name, shape, device):
-    """A device tensor of 32-bit whole numbers of that shape (None: any size)."""
-    _need(t, name, (torch.int32,), len(shape))
-    if any(w is not None and w != g for w, g in zip(shape, t.shape)):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call on {device}")
-    return t
+def _kv_state(table, lengths, refs, pages, index):
+    t = _tensor(table, "table", torch.int32, (None, None), index)
+    seqs, width = table.shape
+    return KvState(t, _tensor(lengths, "lengths", torch.int32, (seqs,), index),
+                   None if refs is None else _tensor(refs, "refs", torch.int32, (pages,), index), seqs, width)
 
 
-def _kv_state(table, lengths, refs, pages, device):
-    _i32(table, "table", (None, None), device)
-    _i32(lengths, "lengths", (table.shape[0],), device)
-    if refs is not None:
-        _i32(refs, "refs", (pages,), device)
-    return KvState(table.data_ptr(), lengths.data_ptr(), None if refs is None else refs.data_ptr(), table.shape[0],
-                   table.shape[1])
-
-
-def _head_rows(t, name, heads, head_dim, dtype, device):
-    """[tokens, heads, D] whose rows may be a view of a wider tensor; its row stride."""
+def _head_rows(t, name, heads, head_dim, dtype, index):
+    """Address and row stride of [tokens, heads, D] whose rows may be a view of a wider tensor."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, the cache holds {dtype}")
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != head_dim:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [tokens, {heads or 'heads'}, {head_dim}]")
-    if t.device != device or t.device.type != "cuda":
-        raise ValueError(f"{name} must be a device tensor on {device}")
-    row = t.shape[1] * head_dim
-    if t.shape[0] < 1 or t.shape[1] < 1:
-        return row
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != head_dim):
+    shape = t.shape
+    if len(shape) != 3 or (heads is not None and shape[1] != heads) or shape[2] != head_dim:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected [tokens, {heads or 'heads'}, {head_dim}]")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be a device tensor on the device of the call, is on {t.device}")
+    n, h, _ = shape
+    row, along, one = t.stride()
+    if n and h and (one != 1 or (h > 1 and along != head_dim)):
         raise ValueError(f"{name}: the heads of a row must be contiguous, got strides {t.stride()}")
-    return t.stride(0) if t.shape[0] > 1 else row
+    return t.data_ptr(), row if n > 1 else h * head_dim
 
 
 def qk_norm_rope(q, k, v, q_weight, k_weight, positions, inv_freq, slots, k_cache, v_cache, eps=1e-6,
@@ -562,44 +617,41 @@ def qk_norm_rope(q, k, v, q_weight, k_weight, positions, inv_freq, slots, k_cach
     first 2 * len(inv_freq) dimensions by positions * inv_freq, and the append
     of k and v to the cache at `slots` (int32 [N], -1: not cached).  q, k and v
     may be views of one projection output.  Returns the queries [N, Hq, D]."""
-    cache = _kv_cache(k_cache, v_cache, False)
-    dev, D, dt = k_cache.device, cache.head_dim, k_cache.dtype
-    qs = _head_rows(q, "q", None, D, dt, dev)
-    ks = _head_rows(k, "k", cache.heads, D, dt, dev)
-    vs = _head_rows(v, "v", cache.heads, D, dt, dev)
-    N = q.shape[0]
+    cache, dev = _kv_cache(k_cache, v_cache, False)
+    D, dt, i32 = cache.head_dim, k_cache.dtype, torch.int32
+    qp, qs = _head_rows(q, "q", None, D, dt, dev)
+    kp, ks = _head_rows(k, "k", cache.heads, D, dt, dev)
+    vp, vs = _head_rows(v, "v", cache.heads, D, dt, dev)
+    N, hq = q.shape[0], q.shape[1]
     if k.shape[0] != N or v.shape[0] != N:
         raise ValueError(f"q, k and v have {N}, {k.shape[0]} and {v.shape[0]} tokens")
-    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        _need(t, name, (dt,), 1)
-        if t.numel() != D:
-            raise ValueError(f"{name} has {t.numel()} entries, a head has {D}")
-    _need(inv_freq, "inv_freq", (torch.float32,), 1)
-    _i32(positions, "positions", (N,), dev)
-    _i32(slots, "slots", (N,), dev)
-    out = _out(out, "out", (N, q.shape[1], D), (dt,), dev)
-    with torch.cuda.device(dev):
-        _check(load_library().trellis_qk_norm_rope(
-            _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq),
-            2 * inv_freq.numel(), int(interleaved), eps, _ptr(slots), _ptr(out), ctypes.byref(cache), N, q.shape[1],
-            _stream(dev)))
+    wq = _tensor(q_weight, "q_weight", dt, (D,), dev)
+    wk = _tensor(k_weight, "k_weight", dt, (D,), dev)
+    inv = _tensor(inv_freq, "inv_freq", torch.float32, (None,), dev)
+    pos = _tensor(positions, "positions", i32, (N,), dev)
+    at = _tensor(slots, "slots", i32, (N,), dev)
+    out, op = _result(out, "out", (N, hq, D), dt, k_cache.device, dev)
+    _call(load_library().trellis_qk_norm_rope, dev, qp, qs, kp, ks, vp, vs, wq, wk, pos, inv, 2 * inv_freq.shape[0],
+          interleaved, eps, at, op, _byref(cache), N, hq)
     return out
 
 
-def _attention(q, k_cache, v_cache, table, lengths, q_start, max_q, scale, seq_ids, out):
-    """what the two attention calls share: (cache, state, entries, row stride, scale, out)"""
-    cache = _kv_cache(k_cache, v_cache, False)
-    dev = k_cache.device
-    stride = _head_rows(q, "q", None, cache.head_dim, k_cache.dtype, dev)
+def _attention(q, k_cache, v_cache, table, lengths, q_start, seq_ids, out):
+    """What the two attention calls share: (device number, q's address and stride, cache, state, addresses of seq_ids,
+    q_start and out, entries, out)."""
+    cache, dev = _kv_cache(k_cache, v_cache, False)
+    dt = k_cache.dtype
+    qp, stride = _head_rows(q, "q", None, cache.head_dim, dt, dev)
     state = _kv_state(table, lengths, None, cache.pages, dev)
-    _i32(q_start, "q_start", (None,), dev)
-    n = q_start.numel() - 1
+    starts = _tensor(q_start, "q_start", torch.int32, (None,), dev)
+    n = q_start.shape[0] - 1
+    ids = None
     if seq_ids is not None:
-        _i32(seq_ids, "seq_ids", (n,), dev)
-    elif n > table.shape[0]:
-        raise ValueError(f"q_start has {n} entries, the table {table.shape[0]} sequences")
-    out = _out(out, "out", tuple(q.shape), (k_cache.dtype,), dev)
-    return cache, state, n, stride, cache.head_dim ** -0.5 if scale is None else scale, out
+        ids = _tensor(seq_ids, "seq_ids", torch.int32, (n,), dev)
+    elif n > state.seqs:
+        raise ValueError(f"q_start has {n} entries, the table {state.seqs} sequences")
+    out, op = _result(out, "out", tuple(q.shape), dt, k_cache.device, dev)
+    return dev, qp, stride, cache, state, ids, starts, op, n, out
 
 
 def tree_attention(q, k_cache, v_cache, table, lengths, q_start, ancestors, max_q, scale=None, seq_ids=None, out=None,
@@ -609,18 +661,15 @@ def tree_attention(q, k_cache, v_cache, table, lengths, q_start, ancestors, max_
     q_start[e+1]-1, at most max_q (<= 64) of them, cached behind `lengths`.
     ancestors int64 [N]: bit m set if the row sees the entry's token m.  scale
     defaults to D ** -0.5.  Returns [N, Hq, D]."""
-    cache, state, n, stride, scale, out = _attention(q, k_cache, v_cache, table, lengths, q_start, max_q, scale,
-                                                     seq_ids, out)
-    _need(ancestors, "ancestors", (torch.int64,), 1)
-    if ancestors.numel() != q.shape[0] or ancestors.device != q.device:
-        raise ValueError(f"ancestors has {ancestors.numel()} entries on {ancestors.device}, q {q.shape[0]} rows")
-    lib, c, s = load_library(), ctypes.byref(cache), ctypes.byref(state)
-    with torch.cuda.device(q.device):
-        need = lib.trellis_tree_attention_workspace_bytes(c, s, n, q.shape[0], q.shape[1], max_q)
-        ws, wsb = _workspace(need, q.device, workspace)
-        _check(lib.trellis_tree_attention(_ptr(q), stride, c, s, _ptr(seq_ids), n, _ptr(q_start), _ptr(ancestors),
-                                          q.shape[0], q.shape[1], max_q, scale, _ptr(out), _ptr(ws), wsb,
-                                          _stream(q.device)))
+    dev, qp, stride, cache, state, ids, starts, op, n, out = _attention(q, k_cache, v_cache, table, lengths, q_start,
+                                                                        seq_ids, out)
+    tokens, hq, D = q.shape
+    anc = _tensor(ancestors, "ancestors", torch.int64, (tokens,), dev)
+    lib, c, s = load_library(), _byref(cache), _byref(state)
+    _keep, ws, wsb = _scratch(lib.trellis_tree_attention_workspace_bytes(c, s, n, tokens, hq, max_q), q.device,
+                              workspace)
+    _call(lib.trellis_tree_attention, dev, qp, stride, c, s, ids, n, starts, anc, tokens, hq, max_q,
+          D ** -0.5 if scale is None else scale, op, ws, wsb)
     return out
 
 
@@ -629,15 +678,14 @@ def window_attention(q, k_cache, v_cache, table, lengths, q_start, max_q, window
     """Causal attention of new tokens over the cache: the token at position p
     sees the keys j <= p with p - j < window (0: no limit) or j < sinks.
     Arguments otherwise as tree_attention; max_q has no upper bound."""
-    cache, state, n, stride, scale, out = _attention(q, k_cache, v_cache, table, lengths, q_start, max_q, scale,
-                                                     seq_ids, out)
-    lib, c, s = load_library(), ctypes.byref(cache), ctypes.byref(state)
-    with torch.cuda.device(q.device):
-        need = lib.trellis_window_attention_workspace_bytes(c, s, n, q.shape[0], q.shape[1], max_q, window, sinks)
-        ws, wsb = _workspace(need, q.device, workspace)
-        _check(lib.trellis_window_attention(_ptr(q), stride, c, s, _ptr(seq_ids), n, _ptr(q_start), q.shape[0],
-                                            q.shape[1], max_q, window, sinks, scale, _ptr(out), _ptr(ws), wsb,
-                                            _stream(q.device)))
+    dev, qp, stride, cache, state, ids, starts, op, n, out = _attention(q, k_cache, v_cache, table, lengths, q_start,
+                                                                        seq_ids, out)
+    tokens, hq, D = q.shape
+    lib, c, s = load_library(), _byref(cache), _byref(state)
+    _keep, ws, wsb = _scratch(lib.trellis_window_attention_workspace_bytes(c, s, n, tokens, hq, max_q, window, sinks),
+                              q.device, workspace)
+    _call(lib.trellis_window_attention, dev, qp, stride, c, s, ids, n, starts, tokens, hq, max_q, window, sinks,
+          D ** -0.5 if scale is None else scale, op, ws, wsb)
     return out
 
 
@@ -653,43 +701,45 @@ def kv_state(seqs, width, pages, device="cuda"):
             torch.zeros(seqs, dtype=torch.int32, device=device), torch.zeros(pages, dtype=torch.int32, device=device))
 
 
+def _state_only(table, lengths, refs, page_size):
+    """(cache without pools, state, device number) of the calls that touch no keys or values"""
+    dev = _index(refs, "refs")
+    if refs.dim() != 1:
+        raise ValueError(f"refs: expected [pages], got shape {tuple(refs.shape)}")
+    pages = refs.shape[0]
+    return KvCache(None, None, pages, 1, 1, 64, page_size, KV_BF16), _kv_state(table, lengths, refs, pages, dev), dev
+
+
 def cache_reserve(table, lengths, refs, page_size, seq_ids, q_start, tokens, slots=None, granted=None, workspace=None):
     """Slots for new tokens: entry b wants q_start[b+1] - q_start[b] tokens behind
     sequence seq_ids[b]; `tokens` in all.  Missing pages are taken from the free
     ones, lowest first.  Returns (slots int32 [tokens], -1 where refused,
     granted int32 [n])."""
-    _need(refs, "refs", (torch.int32,), 1)
-    dev, pages = refs.device, refs.numel()
-    state = _kv_state(table, lengths, refs, pages, dev)
-    cache = KvCache(None, None, pages, 1, 1, 64, page_size, KV_BF16)
-    _i32(seq_ids, "seq_ids", (None,), dev)
-    n = seq_ids.numel()
-    _i32(q_start, "q_start", (n + 1,), dev)
-    slots = _out(slots, "slots", (tokens,), (torch.int32,), dev)
-    granted = _out(granted, "granted", (n,), (torch.int32,), dev)
-    lib, c, s = load_library(), ctypes.byref(cache), ctypes.byref(state)
-    with torch.cuda.device(dev):
-        ws, wsb = _workspace(lib.trellis_cache_reserve_workspace_bytes(c, s, n), dev, workspace)
-        _check(lib.trellis_cache_reserve(c, s, _ptr(seq_ids), n, _ptr(q_start), tokens, _ptr(slots), _ptr(granted),
-                                         _ptr(ws), wsb, _stream(dev)))
+    cache, state, dev = _state_only(table, lengths, refs, page_size)
+    i32, device = torch.int32, refs.device
+    ids = _tensor(seq_ids, "seq_ids", i32, (None,), dev)
+    n = seq_ids.shape[0]
+    starts = _tensor(q_start, "q_start", i32, (n + 1,), dev)
+    slots, sp = _result(slots, "slots", (tokens,), i32, device, dev)
+    granted, gp = _result(granted, "granted", (n,), i32, device, dev)
+    lib, c, s = load_library(), _byref(cache), _byref(state)
+    _keep, ws, wsb = _scratch(lib.trellis_cache_reserve_workspace_bytes(c, s, n), device, workspace)
+    _call(lib.trellis_cache_reserve, dev, c, s, ids, n, starts, tokens, sp, gp, ws, wsb)
     return slots, granted
 
 
 def cache_fork(k_cache, v_cache, table, lengths, refs, parents, children, granted=None, workspace=None):
     """children[b] becomes a copy of parents[b]: full pages shared, the last
     partial page copied in every layer.  Returns granted int32 [n]."""
-    cache = _kv_cache(k_cache, v_cache, True)
-    dev = k_cache.device
+    cache, dev = _kv_cache(k_cache, v_cache, True)
     state = _kv_state(table, lengths, refs, cache.pages, dev)
-    _i32(parents, "parents", (None,), dev)
-    n = parents.numel()
-    _i32(children, "children", (n,), dev)
-    granted = _out(granted, "granted", (n,), (torch.int32,), dev)
-    lib, c, s = load_library(), ctypes.byref(cache), ctypes.byref(state)
-    with torch.cuda.device(dev):
-        ws, wsb = _workspace(lib.trellis_cache_fork_workspace_bytes(c, s, n), dev, workspace)
-        _check(lib.trellis_cache_fork(c, s, _ptr(parents), _ptr(children), n, _ptr(granted), _ptr(ws), wsb,
-                                      _stream(dev)))
+    par = _tensor(parents, "parents", torch.int32, (None,), dev)
+    n = parents.shape[0]
+    kid = _tensor(children, "children", torch.int32, (n,), dev)
+    granted, gp = _result(granted, "granted", (n,), torch.int32, k_cache.device, dev)
+    lib, c, s = load_library(), _byref(cache), _byref(state)
+    _keep, ws, wsb = _scratch(lib.trellis_cache_fork_workspace_bytes(c, s, n), k_cache.device, workspace)
+    _call(lib.trellis_cache_fork, dev, c, s, par, kid, n, gp, ws, wsb)
     return granted
 
 
@@ -697,28 +747,21 @@ def cache_accept(k_cache, v_cache, table, lengths, seq_ids, path, counts, new_le
     """Drafted rows path[b][: counts[b]] of sequence seq_ids[b] move up behind its
     cached tokens in every layer; lengths grows by counts (in place, or into
     new_lengths).  Returns the new lengths."""
-    cache = _kv_cache(k_cache, v_cache, True)
-    dev = k_cache.device
-    state = _kv_state(table, lengths, None, cache.pages, dev)
-    _i32(seq_ids, "seq_ids", (None,), dev)
-    n = seq_ids.numel()
-    _i32(path, "path", (n, None), dev)
-    _i32(counts, "counts", (n,), dev)
-    new_lengths = lengths if new_lengths is None else _i32(new_lengths, "new_lengths", (table.shape[0],), dev)
-    with torch.cuda.device(dev):
-        _check(load_library().trellis_cache_accept(ctypes.byref(cache), ctypes.byref(state), _ptr(seq_ids), n,
-                                                   _ptr(path), path.shape[1], _ptr(counts), _ptr(new_lengths),
-                                                   _stream(dev)))
+    cache, dev = _kv_cache(k_cache, v_cache, True)
+    state, i32 = _kv_state(table, lengths, None, cache.pages, dev), torch.int32
+    ids = _tensor(seq_ids, "seq_ids", i32, (None,), dev)
+    n = seq_ids.shape[0]
+    pp = _tensor(path, "path", i32, (n, None), dev)
+    cp = _tensor(counts, "counts", i32, (n,), dev)
+    if new_lengths is None:
+        new_lengths = lengths
+    to = _tensor(new_lengths, "new_lengths", i32, (state.seqs,), dev)
+    _call(load_library().trellis_cache_accept, dev, _byref(cache), _byref(state), ids, n, pp, path.shape[1], cp, to)
     return new_lengths
 
 
 def cache_free(table, lengths, refs, seq_ids):
     """The pages of the listed sequences are returned; their rows become empty."""
-    _need(refs, "refs", (torch.int32,), 1)
-    dev = refs.device
-    state = _kv_state(table, lengths, refs, refs.numel(), dev)
-    _i32(seq_ids, "seq_ids", (None,), dev)
-    cache = KvCache(None, None, refs.numel(), 1, 1, 64, 16, KV_BF16)
-    with torch.cuda.device(dev):
-        _check(load_library().trellis_cache_free(ctypes.byref(cache), ctypes.byref(state), _ptr(seq_ids),
-                                                 seq_ids.numel(), _stream(dev)))
+    cache, state, dev = _state_only(table, lengths, refs, 16)
+    ids = _tensor(seq_ids, "seq_ids", torch.int32, (None,), dev)
+    _call(load_library().trellis_cache_free, dev, _byref(cache), _byref(state), ids, seq_ids.shape[0])
