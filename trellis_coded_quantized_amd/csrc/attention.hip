@@ -11,7 +11,7 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kFewRows = 32;              // rows of the few-row kernel: one MFMA tile
 constexpr int kManyRows = 128;            // rows of a many-row workgroup: 32 a wave
-constexpr int kManyKeys = 64;             // keys of one of its tiles
+constexpr int kManyKeys = 64;             // keys of a tile of the many-row kernel
 
 // ---- few rows ------------------------------------------------------------
 // All rows of an entry that share a key head (tokens x query heads per key
@@ -76,7 +76,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_few_kern
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const Unit u = find_unit<TREE>(a, blockIdx.x, false);
   if (!u.live) return;
-  const Entry e = load_entry(a, u.e);
+  const Entry e = uniform(load_entry(a, u.e));
   const int h = blockIdx.y, group = a.heads_q / a.heads_kv, rows = e.n * group;
   const TileList list = tile_list<32, TREE>(a, e, 0, e.n - 1);
   const int t0 = u.split * u.chunk, t1 = min(list.count, t0 + u.chunk);
@@ -85,6 +85,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_few_kern
   const bool live = col < rows;
   const int i = live ? col / group : 0, hq = h * group + (live ? col % group : 0);
   const RowMask mask = row_mask<TREE>(a, e, i, live);
+  const OpenKeys seen_by_all = open_keys<TREE>(a, e, 0, e.n - 1);
   u32x4v q[STEPS];
   {
     const uint16_t* src = a.q + (int64_t)(e.first + i) * a.q_stride + (int64_t)hq * D + half * 8;
@@ -120,21 +121,16 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_few_kern
     f32x16 sc[1] = {f32x16{}};
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) sc[0] = T::mfma(kf[s], q[s], sc[0]);
-    const bool open = tile_open<32, TREE>(a, e, 0, e.n - 1, kb);
-    if (!open) {
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int key = kb + (r >> 3) * 16 + half * 8 + (r & 7);
-        if (!mask.sees<TREE>(key)) sc[0][r] = -INFINITY;
-      }
-    }
+    const bool open = seen_by_all.tile(kb, 32);
+    if (!open) cut_scores(sc[0], (uint32_t)mask.bits<TREE>(kb));
     float alpha;
-    if (softmax_step(sc, c, st, alpha)) {
+    if (move_bound(sc, c, st, alpha)) {
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[d][r] *= alpha;
     }
+    weigh(sc, c, st);
     bool bad = false;
     if (!open) {
 #pragma unroll
@@ -148,7 +144,9 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_few_kern
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int s = 0; s < 2; ++s) o[d] = T::mfma(vf[s][d], p[s], o[d]);
-    if (__any(bad)) add_nonfinite<T, D, TREE>(a, e, mask, h, kb, 32, o);
+    if (__any(bad))
+      add_nonfinite<T, D, TREE>(a.v + h * head_elems, e.pages, a.pages, (uint32_t)(a.heads_kv * head_elems),
+                                a.page_log2, mask, kb, 32, o);
   }
 
   // join the four waves
@@ -203,6 +201,23 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_few_kern
 // innermost), 32 a wave, and walks its keys in tiles of 64 that all waves
 // share through LDS, in the cache's own granule order, so LDS reads are
 // contiguous across lanes and nothing is transposed.
+//
+// A tile is two blocks of 32 keys.  The second block's scores are computed
+// under the first block's exponentials, and the first block's product with the
+// values under the second's: the vector work of the softmax (over half of it
+// exponentials) is about as long as the matrix instructions at D = 128.
+
+// Let every matrix instruction of a block be followed by vector ones (a
+// scheduling hint for the code around it).
+template <int MFMAS, int VALU, int TRANS>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int i = 0; i < MFMAS; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+    __builtin_amdgcn_sched_group_barrier(0x400, TRANS, 0);
+  }
+}
 
 template <typename T, int D, bool TREE>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_many_kernel(AttnArgs a) {
@@ -215,7 +230,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_many_ker
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int split = blockIdx.x % a.splits, rt = gridDim.x / a.splits - 1 - blockIdx.x / a.splits;
   const int h = blockIdx.y, group = a.heads_q / a.heads_kv;
-  const Entry e = load_entry(a, blockIdx.z);
+  const Entry e = uniform(load_entry(a, blockIdx.z));
   const int rows = e.n * group, r0 = rt * kManyRows;
   if (r0 >= rows) return;
   const int i0 = r0 / group, i1 = min(e.n - 1, (r0 + kManyRows - 1) / group);
@@ -223,12 +238,13 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_many_ker
   const int chunk = (list.count + a.splits - 1) / a.splits;
   const int t0 = split * chunk, t1 = min(list.count, t0 + chunk);
   const int P = 1 << a.page_log2, pmask = P - 1;
-  const int64_t head_elems = (int64_t)D << a.page_log2;
 
   const int row = r0 + wave * 32 + col;
   const bool live = row < rows;
   const int i = live ? row / group : 0, hq = h * group + (live ? row % group : 0);
   const RowMask mask = row_mask<TREE>(a, e, i, live);
+  const OpenKeys seen_by_all = open_keys<TREE>(a, e, i0, i1);
+  const bool wave_live = r0 + wave * 32 < rows;              // else it only carries tiles
   u32x4v q[STEPS];
   {
     const uint16_t* src = a.q + (int64_t)(e.first + i) * a.q_stride + (int64_t)hq * D + half * 8;
@@ -241,103 +257,127 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_many_ker
   Running st{-INFINITY, 0.0f};
   const float c = a.scale * kLog2e;
 
-  u32x4v kin[PER], vin[PER];
+  u32x4v in[PER];                                            // a thread's granules of one operand on their way
   // The page of each of a tile's keys, one key a lane.
   auto pages_of = [&](int t) {
     const int key = list.key<KT>(min(t, t1 - 1)) + lane;
     return e.pages[min(key >> a.page_log2, (int)a.width - 1)];
   };
+  const uint32_t page_elems = (uint32_t)(a.heads_kv * D) << a.page_log2, head_at = (uint32_t)(h * D) << a.page_log2;
   // keys: granule g of the tile is dimension block g / 64 of key g % 64, so
-  // a thread keeps its key; values: granule g is token block g / D of
-  // dimension g % D, one token block a wave.
-  auto fetch = [&](int t, int32_t pk) {
-    const int kb = list.key<KT>(t);
-    const uint16_t* kp = a.k + ((int64_t)page_in_pool(pk, a.pages) * a.heads_kv + h) * head_elems +
-                         ((kb + lane) & pmask) * 8 + (int64_t)wave * P * 8;
+  // a thread keeps its key
+  auto fetch_keys = [&](int t, int32_t pk) {
+    const uint16_t* kp = a.k + (uint64_t)page_in_pool(pk, a.pages) * page_elems + head_at +
+                         (((list.key<KT>(t) + lane) & pmask) + wave * P) * 8;
 #pragma unroll
-    for (int n = 0; n < PER; ++n) kin[n] = *reinterpret_cast<const u32x4v*>(kp + (int64_t)n * kWaves * P * 8);
+    for (int n = 0; n < PER; ++n) in[n] = *reinterpret_cast<const u32x4v*>(kp + n * kWaves * P * 8);
+  };
+  // values: granule g is token block g / D of dimension g % D, one token
+  // block a wave, whose address the lane of the block's first key works out
+  auto fetch_values = [&](int t, int32_t pk) {
+    const uint64_t block = (uint64_t)(a.v + (uint64_t)page_in_pool(pk, a.pages) * page_elems + head_at +
+                                      (((list.key<KT>(t) + lane) & pmask) >> 3) * D * 8);
 #pragma unroll
     for (int n = 0; n < PER; ++n) {
-      const int g = n * kThreads + wave * 64, tg = g / D, first = kb + tg * 8;
-      const int32_t pv = __builtin_amdgcn_readlane(pk, tg * 8);
-      const uint16_t* vp = a.v + ((int64_t)page_in_pool(pv, a.pages) * a.heads_kv + h) * head_elems +
-                           (int64_t)((first & pmask) >> 3) * D * 8 + (g % D) * 8;
-      vin[n] = *reinterpret_cast<const u32x4v*>(vp + lane * 8);
+      const int g = n * kThreads + wave * 64, at = g / D * 8;
+      const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)block, at);
+      const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(block >> 32), at);
+      in[n] = reinterpret_cast<const __attribute__((address_space(1))) u32x4v*>(((uint64_t)hi << 32) | lo)[g % D + lane];
     }
   };
+  auto store_keys = [&](int buf) {
+#pragma unroll
+    for (int n = 0; n < PER; ++n) lds[buf * 2 * GRAN + n * kThreads + tid] = in[n];
+  };
   // s_bad: the last tile whose values had to be cleaned
-  auto store = [&](int buf, int t) {
-    u32x4v* dst = lds + buf * 2 * GRAN;
-    if (!tile_open<KT, TREE>(a, e, i0, i1, list.key<KT>(t))) {
+  auto store_values = [&](int buf, int t) {
+    if (!seen_by_all.tile(list.key<KT>(t), KT)) {
       bool bad = false;
 #pragma unroll
-      for (int n = 0; n < PER; ++n) bad |= drop_nonfinite<T>(vin[n]);
+      for (int n = 0; n < PER; ++n) bad |= drop_nonfinite<T>(in[n]);
       if (bad) s_bad[buf] = t;
     }
 #pragma unroll
-    for (int n = 0; n < PER; ++n) {
-      dst[n * kThreads + tid] = kin[n];
-      dst[GRAN + n * kThreads + tid] = vin[n];
-    }
+    for (int n = 0; n < PER; ++n) lds[(buf * 2 + 1) * GRAN + n * kThreads + tid] = in[n];
+  };
+  auto rescale = [&](float alpha) {
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[d][r] *= alpha;
   };
 
   if (tid < 2) s_bad[tid] = -1;
   lds_barrier();
-  int32_t next = 0;
+  int32_t page = 0;
   if (t0 < t1) {
-    fetch(t0, pages_of(t0));
-    next = pages_of(t0 + 1);
-    store(0, t0);
+    page = pages_of(t0);
+    fetch_keys(t0, page);
+    store_keys(0);
+    fetch_values(t0, page);
+    page = pages_of(t0 + 1);
+    store_values(0, t0);
   }
   lds_barrier();
   const int krow = tile_key_of_row(col);
+  waitcnt_vm<0>();         // q has arrived: waits inside the loop are for the tiles' loads only
   for (int t = t0; t < t1; ++t) {
     const int buf = (t - t0) & 1, kb = list.key<KT>(t);
-    const u32x4v* kt = lds + buf * 2 * GRAN;
-    const u32x4v* vt = kt + GRAN;
-    if (t + 1 < t1) {
-      fetch(t + 1, next);
-      next = pages_of(t + 2);
-    }
-    f32x16 sc[2] = {f32x16{}, f32x16{}};
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) sc[x] = T::mfma(kt[(2 * s + half) * KT + x * 32 + krow], q[s], sc[x]);
-    if (!tile_open<KT, TREE>(a, e, i0, i1, kb)) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int key = kb + x * 32 + (r >> 3) * 16 + half * 8 + (r & 7);
-          if (!mask.sees<TREE>(key)) sc[x][r] = -INFINITY;
-        }
-    }
+    const bool more = t + 1 < t1;
+    const u32x4v* kt = lds + buf * 2 * GRAN + half * KT + krow;        // [2 s + half][32 x + key]
+    const u32x4v* vt = lds + (buf * 2 + 1) * GRAN + half * D + col;    // [4 x + 2 s + half][dimension]
+    if (more) fetch_keys(t + 1, page);
+    const bool open = seen_by_all.tile(kb, KT);
+    uint64_t seen = 0;
+    f32x16 s0[1] = {f32x16{}}, s1[1] = {f32x16{}};
+    u32x4v p0[2], p1[2];
     float alpha;
-    if (softmax_step(sc, c, st, alpha)) {
+    bool moved = false;
+    if (wave_live) {
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
+      for (int s = 0; s < STEPS; ++s) s0[0] = T::mfma(kt[2 * s * KT], q[s], s0[0]);
+      if (!open) {
+        seen = mask.bits<TREE>(kb);
+        cut_scores(s0[0], (uint32_t)seen);
+      }
+      if (move_bound(s0, c, st, alpha)) rescale(alpha);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) o[d][r] *= alpha;
+      for (int s = 0; s < STEPS; ++s) s1[0] = T::mfma(kt[2 * s * KT + 32], q[s], s1[0]);
+      weigh(s0, c, st);
+      pack_weights<T>(s0[0], p0);
+      interleave<STEPS, 56 / STEPS, 16 / STEPS>();
     }
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      u32x4v p[2];
-      pack_weights<T>(sc[x], p);
+    if (more) {
+      store_keys(buf ^ 1);
+      fetch_values(t + 1, page);
+      page = pages_of(t + 2);
+    }
+    if (wave_live) {
+      if (!open) cut_scores(s1[0], (uint32_t)(seen >> 32));
+      moved = move_bound(s1, c, st, alpha);
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int d = 0; d < DT; ++d) o[d] = T::mfma(vt[(x * 4 + 2 * s + half) * D + d * 32 + col], p[s], o[d]);
+        for (int d = 0; d < DT; ++d) o[d] = T::mfma(vt[2 * s * D + d * 32], p0[s], o[d]);
+      weigh(s1, c, st);
+      pack_weights<T>(s1[0], p1);
+      interleave<2 * DT, 56 / (2 * DT), 16 / (2 * DT)>();
+      if (moved) rescale(alpha);                             // the first block was weighed with the earlier bound
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[d] = T::mfma(vt[(4 + 2 * s) * D + d * 32], p1[s], o[d]);
+      if (!open && s_bad[buf] == t)
+        add_nonfinite<T, D, TREE>(a.v + head_at, e.pages, a.pages, page_elems, a.page_log2, mask, kb, KT, o);
     }
-    if (s_bad[buf] == t) add_nonfinite<T, D, TREE>(a, e, mask, h, kb, KT, o);
-    if (t + 1 < t1) store(buf ^ 1, t + 1);
+    if (more) store_values(buf ^ 1, t + 1);
     lds_barrier();
   }
 
-  st.l += __shfl_xor(st.l, 32);
+  const float l = st.l + __shfl_xor(st.l, 32);
   if (!live) return;
   if (a.splits == 1) {
-    const float inv = st.l == 0.0f ? 0.0f : 1.0f / st.l;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     uint16_t* dst = a.out + ((int64_t)(e.first + i) * a.heads_q + hq) * D + 4 * half;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
@@ -348,7 +388,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_many_ker
     return;
   }
   const int64_t at = ((int64_t)(e.first + i) * a.heads_q + hq) * a.splits + split;
-  if (half == 0) *reinterpret_cast<f32x2p*>(a.part_ml + at * 2) = f32x2p{st.m, st.l};
+  if (half == 0) *reinterpret_cast<f32x2p*>(a.part_ml + at * 2) = f32x2p{st.m, l};
   if (st.m == -INFINITY) return;
   float* part = a.part_o + at * D + 4 * half;
 #pragma unroll

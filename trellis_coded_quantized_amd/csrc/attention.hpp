@@ -25,6 +25,9 @@
 
 namespace trellis {
 
+// an address known to be in device memory (a pointer put together from integers is not)
+typedef const __attribute__((address_space(1))) int32_t* GlobalInts;
+
 constexpr float kLog2e = 1.4426950408889634f;
 // The bound m follows the row maximum only when that has grown by more than
 // 2^8: weights stay below 2^8 (finite in fp16, the same relative precision),
@@ -41,7 +44,7 @@ struct Entry {
   int first, n;        // rows of q
   int ctx;             // tokens cached before this call
   int total;           // keys with storage: ctx + n, at most the table's
-  const int32_t* pages;
+  GlobalInts pages;
 };
 
 __device__ __forceinline__ Entry load_entry(const AttnArgs& a, int e) {
@@ -57,8 +60,21 @@ __device__ __forceinline__ Entry load_entry(const AttnArgs& a, int e) {
   r.n = known ? min(f - b, a.max_q) : 0;
   r.ctx = (int)min((int64_t)max(len, 0), room);
   r.total = (int)min((int64_t)r.ctx + r.n, room);
-  r.pages = a.table + (known ? row : 0) * a.width;
+  r.pages = (GlobalInts)(a.table + (known ? row : 0) * a.width);
   return r;
+}
+
+// The same entry with its numbers in scalar registers (all lanes hold the same).
+__device__ __forceinline__ Entry uniform(Entry e) {
+  e.first = __builtin_amdgcn_readfirstlane(e.first);
+  e.n = __builtin_amdgcn_readfirstlane(e.n);
+  e.ctx = __builtin_amdgcn_readfirstlane(e.ctx);
+  e.total = __builtin_amdgcn_readfirstlane(e.total);
+  const uint64_t p = (uint64_t)e.pages;
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32));
+  e.pages = (GlobalInts)(((uint64_t)hi << 32) | lo);
+  return e;
 }
 
 // The key tiles (of KT keys) that tokens i0 .. i1 of an entry read, as a
@@ -95,15 +111,32 @@ __device__ __forceinline__ TileList tile_list(const AttnArgs& a, const Entry& e,
 struct RowMask {
   int below, from, sinks;
   uint64_t nodes;
+  // bit j: key kb + j (of 64) is seen
   template <bool TREE>
-  __device__ __forceinline__ bool sees(int key) const {
+  __device__ __forceinline__ uint64_t bits(int kb) const {
+    const uint64_t under = ones(below - kb);
     if (TREE) {
-      const int m = key - below;
-      return m < 0 || (m < 64 && ((nodes >> (m & 63)) & 1));
+      const int at = below - kb;                             // where node 0 stands
+      const uint64_t drafted = at >= 64 || at <= -64 ? 0 : at >= 0 ? nodes << at : nodes >> -at;
+      return under | drafted;
     }
-    return key < below && (key >= from || key < sinks);
+    return under & (~ones(from - kb) | ones(sinks - kb));
+  }
+  // the n lowest bits
+  static __device__ __forceinline__ uint64_t ones(int n) {
+    return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
   }
 };
+
+// Scores of keys that the row does not see become -inf.  `seen`: bits of the
+// 32-key tile; a lane half holds keys 16 s + 8 half + 0 .. 7 in accumulators
+// 8 s + 0 .. 7.
+__device__ __forceinline__ void cut_scores(f32x16& s, uint32_t seen) {
+  asm volatile("" : "+v"(seen));          // keeps the caller's branch: most tiles need none of this
+  seen >>= ((int)__lane_id() >> 5) * 8;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) s[r] = (seen >> ((r >> 3) * 16 + (r & 7))) & 1u ? s[r] : -INFINITY;
+}
 
 template <bool TREE>
 __device__ __forceinline__ RowMask row_mask(const AttnArgs& a, const Entry& e, int i, bool live) {
@@ -116,24 +149,36 @@ __device__ __forceinline__ RowMask row_mask(const AttnArgs& a, const Entry& e, i
   if (TREE) {
     r.below = e.ctx;
     // bits of nodes that have no token, or no room in the table, see nothing
-    const int room = min(e.total - e.ctx, 64);
-    const uint64_t have = room >= 64 ? ~0ull : ((1ull << room) - 1);
-    r.nodes = (uint64_t)a.ancestors[e.first + i] & have;
+    r.nodes = (uint64_t)a.ancestors[e.first + i] & RowMask::ones(e.total - e.ctx);
   } else {
     const int pos = e.ctx + i;
     r.below = min(pos + 1, e.total);
-    r.from = a.window > 0 ? pos - a.window + 1 : 0;
+    r.from = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
     r.sinks = a.sinks;
   }
   return r;
 }
 
-// Whether keys kb .. kb + KT - 1 are seen by every row of tokens i0 .. i1.
-template <int KT, bool TREE>
-__device__ __forceinline__ bool tile_open(const AttnArgs& a, const Entry& e, int i0, int i1, int kb) {
-  if (TREE) return kb + KT <= e.ctx;
-  if (kb + KT > min(e.ctx + i0 + 1, e.total)) return false;
-  return a.window <= 0 || kb >= e.ctx + i1 - a.window + 1 || kb + KT <= a.sinks;
+// The keys that every row of tokens i0 .. i1 sees: from .. to - 1, and those
+// below sinks.
+struct OpenKeys {
+  int from, to, sinks;
+  __device__ __forceinline__ bool tile(int kb, int keys) const {
+    return kb + keys <= to && (kb >= from || kb + keys <= sinks);
+  }
+};
+
+template <bool TREE>
+__device__ __forceinline__ OpenKeys open_keys(const AttnArgs& a, const Entry& e, int i0, int i1) {
+  if (TREE) return {0, e.ctx, 0};
+  return {a.window > 0 ? max(e.ctx + i1 - a.window + 1, 0) : 0, min(e.ctx + i0 + 1, e.total), a.sinks};
+}
+
+// x and the same of the lane 32 away, the larger of the two.
+__device__ __forceinline__ float max_of_halves(float x) {
+  const uint32_t v = __builtin_bit_cast(uint32_t, x);
+  const auto both = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return fmaxf(__builtin_bit_cast(float, (uint32_t)both[0]), __builtin_bit_cast(float, (uint32_t)both[1]));
 }
 
 // The running softmax of the rows a wave owns.
@@ -142,37 +187,38 @@ struct Running {
   float l;     // sum of weights over this lane's keys
 };
 
-// Scores of NS 32-key tiles -> weights in place (unrounded), and the running
-// bound; `alpha` is what earlier sums and outputs are multiplied with, 1
-// unless `moved` (the same answer in all lanes) is returned.
+// Move the running bound to the scores of NS 32-key tiles.  Returns whether any
+// row of the wave moved; `alpha` is then what the lane's earlier sums (done
+// here) and outputs have to be multiplied with.
 template <int NS>
-__device__ __forceinline__ bool softmax_step(f32x16 (&s)[NS], float c, Running& st, float& alpha) {
+__device__ __forceinline__ bool move_bound(const f32x16 (&s)[NS], float c, Running& st, float& alpha) {
   float top = s[0][0];
 #pragma unroll
   for (int t = 0; t < NS; ++t)
 #pragma unroll
     for (int r = 0; r < 16; ++r) top = fmaxf(top, s[t][r]);
-  top = fmaxf(top, __shfl_xor(top, 32)) * c;
-  const bool grew = top > st.m + kRescaleStep;          // -inf + 8 = -inf: a first visible key grows it
-  const bool moved = __any(grew);
-  alpha = 1.0f;
-  if (moved) {
-    const float m = fmaxf(st.m, top);
-    alpha = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.m - m);
-    st.m = m;
-    st.l *= alpha;
-  }
+  top = max_of_halves(top) * c;
+  if (!__any(top > st.m + kRescaleStep)) return false;   // -inf + 8 = -inf: a first visible key moves it
+  const float m = fmaxf(st.m, top);
+  alpha = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.m - m);
+  st.m = m;
+  st.l *= alpha;
+  return true;
+}
+
+// Scores -> weights in place (unrounded), added to the lane's sum.
+template <int NS>
+__device__ __forceinline__ void weigh(f32x16 (&s)[NS], float c, Running& st) {
   const float bound = st.m == -INFINITY ? 0.0f : st.m;
-  float sum = 0.0f;
+  float sum[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int t = 0; t < NS; ++t)
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       s[t][r] = __builtin_amdgcn_exp2f(fmaf(s[t][r], c, -bound));
-      sum += s[t][r];
+      sum[r & 1] += s[t][r];
     }
-  st.l += sum;
-  return moved;
+  st.l += sum[0] + sum[1];
 }
 
 // The B operands of the second product: weights of one tile, rounded.
@@ -204,21 +250,23 @@ __device__ __forceinline__ bool drop_nonfinite(u32x4v& v) {
 }
 
 template <typename T, int D, bool TREE>
-__device__ __forceinline__ void add_nonfinite(const AttnArgs& a, const Entry& e, const RowMask& mask, int h, int kb,
-                                              int keys, f32x16 (&o)[D / 32]) {
-  const int half = (int)__lane_id() >> 5, P = 1 << a.page_log2;
+__device__ __forceinline__ void add_nonfinite(const uint16_t* v_head, GlobalInts pages, uint32_t pool,
+                                              uint32_t page_elems, int page_log2, const RowMask& mask, int kb, int keys,
+                                              f32x16 (&o)[D / 32]) {
+  const int half = (int)__lane_id() >> 5;
   for (int key = kb; key < kb + keys; ++key) {
-    if (!mask.sees<TREE>(key)) continue;
-    const uint16_t* v = a.v + ((int64_t)page_in_pool(e.pages[key >> a.page_log2], a.pages) * a.heads_kv + h) *
-                                  ((int64_t)D << a.page_log2) +
-                        (int64_t)((key & (P - 1)) >> 3) * D * 8 + (key & 7);
+    const uint16_t* v = v_head + (uint64_t)page_in_pool(pages[key >> page_log2], pool) * page_elems +
+                        ((key & ((1 << page_log2) - 1)) >> 3) * D * 8 + (key & 7);
+    const uint32_t sees = (uint32_t)mask.bits<TREE>(key) & 1u;
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d)
+    for (int d = 0; d < D / 32; ++d) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const uint16_t x = v[(d * 32 + 8 * (r >> 2) + 4 * half + (r & 3)) * 8];
-        if ((x & T::kExp) == T::kExp) o[d][r] += T::to_f32(x);
+        o[d][r] += (x & T::kExp) == T::kExp && sees ? T::to_f32(x) : 0.0f;
       }
+      __builtin_amdgcn_sched_barrier(0);                     // rare code: few registers, not speed
+    }
   }
 }
 
