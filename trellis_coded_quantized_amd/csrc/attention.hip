@@ -10,8 +10,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kFewRows = 32;              // rows of the few-row kernel: one MFMA tile
-constexpr int kManyRows = 128;            // rows of a many-row workgroup: 32 a wave
 constexpr int kManyKeys = 64;             // keys of a tile of the many-row kernel
+constexpr int kManyRun = 4;               // fewest tiles that it cuts the keys into
 
 // ---- few rows ------------------------------------------------------------
 // All rows of an entry that share a key head (tokens x query heads per key
@@ -22,7 +22,7 @@ constexpr int kManyKeys = 64;             // keys of a tile of the many-row kern
 // lengths are.  Every workgroup computes the same cut from the lengths.
 
 struct Unit {
-  int e, split, splits, chunk, base;
+  int e, split, splits, chunk;
   bool live;
 };
 
@@ -34,35 +34,30 @@ __device__ __forceinline__ int entry_tiles(const AttnArgs& a, int e) {
   return max(1, tile_list<32, TREE>(a, en, 0, en.n - 1).count);
 }
 
-// Slot -> (entry, split), or with by_entry: entry -> its slots.
+// Slot -> (entry, split).
 template <bool TREE>
-__device__ __forceinline__ Unit find_unit(const AttnArgs& a, int want, bool by_entry) {
+__device__ __forceinline__ Unit find_unit(const AttnArgs& a, int slot) {
   const int lane = (int)__lane_id();
-  Unit u;
-  u.live = false;
-  u.e = u.split = u.splits = u.base = 0;
+  Unit u{};
   int tiles = entry_tiles<TREE>(a, lane);
   int total = wave_sum(tiles);
   for (int b = 64; b < a.entries; b += 64) total += wave_sum(entry_tiles<TREE>(a, b + lane));
-  u.chunk = max(kWaves, (total + a.target - 1) / a.target);
+  u.chunk = __builtin_amdgcn_readfirstlane(max(kWaves, (total + a.target - 1) / a.target));
   int before = 0;
   for (int b = 0; b < a.entries; b += 64) {
     if (b) tiles = entry_tiles<TREE>(a, b + lane);
     const int parts = (tiles + u.chunk - 1) / u.chunk;
     const int upto = wave_scan_add(parts);
-    const int last = __shfl(upto, 63);
-    const uint64_t hit = by_entry ? (want - b < 64 ? 1ull << (want - b) : 0ull)
-                                  : __ballot(before + upto > want);
+    const uint64_t hit = __ballot(before + upto > slot);
     if (hit) {
       const int at = __builtin_ctzll(hit);
       u.e = b + at;
-      u.splits = __shfl(parts, at);
-      u.base = before + __shfl(upto, at) - u.splits;
-      u.split = by_entry ? 0 : want - u.base;
-      u.live = u.splits > 0;
+      u.splits = __builtin_amdgcn_readfirstlane(__shfl(parts, at));
+      u.split = slot - before - __builtin_amdgcn_readfirstlane(__shfl(upto, at)) + u.splits;
+      u.live = true;
       return u;
     }
-    before += last;
+    before += __builtin_amdgcn_readfirstlane(__shfl(upto, 63));
   }
   return u;
 }
@@ -74,10 +69,14 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_few_kern
   __shared__ __align__(16) float s_o[kWaves][32][36];
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, col = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const Unit u = find_unit<TREE>(a, blockIdx.x, false);
+  const int h = blockIdx.y, group = a.heads_q / a.heads_kv;
+  const Unit u = find_unit<TREE>(a, blockIdx.x);
+  const Entry e = u.live ? uniform(load_entry(a, u.e)) : Entry{};
+  const int rows = e.n * group;
+  if (h == 0 && tid == 0)                                    // for the fold: a split unit's first slot says so
+    a.part_note[blockIdx.x] = u.live && u.split == 0 && u.splits > 1 ? PartNote{u.splits, e.first, rows, 0}
+                                                                     : PartNote{0, 0, 0, 0};
   if (!u.live) return;
-  const Entry e = uniform(load_entry(a, u.e));
-  const int h = blockIdx.y, group = a.heads_q / a.heads_kv, rows = e.n * group;
   const TileList list = tile_list<32, TREE>(a, e, 0, e.n - 1);
   const int t0 = u.split * u.chunk, t1 = min(list.count, t0 + u.chunk);
   const int P = 1 << a.page_log2, pmask = P - 1;
@@ -118,28 +117,28 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_few_kern
 #pragma unroll
       for (int d = 0; d < DT; ++d) vf[s][d] = *reinterpret_cast<const u32x4v*>(vp + d * 256);
     }
-    f32x16 sc[1] = {f32x16{}};
+    f32x16 sc = f32x16{};
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) sc[0] = T::mfma(kf[s], q[s], sc[0]);
+    for (int s = 0; s < STEPS; ++s) sc = T::mfma(kf[s], q[s], sc);
     const bool open = seen_by_all.tile(kb, 32);
-    if (!open) cut_scores(sc[0], (uint32_t)mask.bits<TREE>(kb));
-    float alpha;
-    if (move_bound(sc, c, st, alpha)) {
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) o[d][r] *= alpha;
-    }
-    weigh(sc, c, st);
     bool bad = false;
     if (!open) {
+      cut_scores(sc, (uint32_t)mask.bits<TREE>(kb));
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int d = 0; d < DT; ++d) bad |= drop_nonfinite<T>(vf[s][d]);
     }
+    const float top = row_top(sc, c);
+    if (must_move(top, st)) {
+      const float alpha = move_bound(top, st);
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[d][r] *= alpha;
+    }
     u32x4v p[2];
-    pack_weights<T>(sc[0], p);
+    st.l += weigh<T>(sc, c, st, p);
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -197,255 +196,443 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_few_kern
 }
 
 // ---- many rows -----------------------------------------------------------
-// A workgroup takes 128 rows (token-major, the query heads of one key head
+// A workgroup takes 256 rows (token-major, the query heads of one key head
 // innermost), 32 a wave, and walks its keys in tiles of 64 that all waves
 // share through LDS, in the cache's own granule order, so LDS reads are
-// contiguous across lanes and nothing is transposed.
+// contiguous across lanes and nothing is transposed.  At D = 256 a wave's
+// outputs and queries fill a SIMD's registers alone, and it is 128 rows.
 //
 // A tile is two blocks of 32 keys.  The second block's scores are computed
 // under the first block's exponentials, and the first block's product with the
-// values under the second's: the vector work of the softmax (over half of it
-// exponentials) is about as long as the matrix instructions at D = 128.
+// values under the second's.  (Taking weights under the old bound while the
+// maximum is still being worked out, and again where it moved, measured
+// slower at D = 128: 830 against 908 TFLOP/s.  So did two workgroups of 128
+// rows a compute unit: 821.)
+template <int D>
+struct Many {
+  static constexpr int kWaves = D == 256 ? 4 : 8;
+  static constexpr int kThreads = 64 * kWaves, kRows = 32 * kWaves;
+};
 
-// Let every matrix instruction of a block be followed by vector ones (a
-// scheduling hint for the code around it).
+// Scheduling hint for the code around it: a few operand reads ahead, then every
+// matrix instruction followed by the next read and vector instructions.
 template <int MFMAS, int VALU, int TRANS>
 __device__ __forceinline__ void interleave() {
+  constexpr int AHEAD = 4;
+  __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
 #pragma unroll
   for (int i = 0; i < MFMAS; ++i) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
-    __builtin_amdgcn_sched_group_barrier(0x400, TRANS, 0);
+    if (i < MFMAS - AHEAD) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    if (VALU) __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+    if (TRANS) __builtin_amdgcn_sched_group_barrier(0x400, TRANS, 0);
   }
 }
 
+// Weights that were taken before this point, not where they are used.
+__device__ __forceinline__ void keep_here(u32x4v (&p)[2], float& sum) {
+  asm volatile("" : "+v"(p[0]), "+v"(p[1]), "+v"(sum));
+}
+
+// The work of a key head is the list of its units (entry, row tile), tokens
+// ascending, each as long as the key tiles it reads.  Every workgroup takes an
+// equal run of that list, whatever the lengths and masks are: a run may end
+// inside a unit, and the unit then goes on in the next workgroup.  Parts of
+// units go to the workspace (a workgroup has at most two: the end of a unit it
+// did not begin, in place 0 of its slot, and the beginning of one it does not
+// end, in place 1) and are folded by the kernel after this one; whole units
+// are written by the workgroup that has them.
+
+template <int ROWS>
+__device__ __forceinline__ int row_tiles_of(const Entry& e, int group) {
+  return (e.n * group + ROWS - 1) / ROWS;
+}
+
+// The order of an entry's row tiles in the list: first, last, second, last but
+// one, ...: under a causal mask short and long ones alternate, so no run is
+// made of many short ones (each costs its start and its end).
+__device__ __forceinline__ int row_tile_at(int u, int rts) { return u & 1 ? rts - 1 - (u >> 1) : u >> 1; }
+
+template <int ROWS, bool TREE>
+__device__ __forceinline__ int unit_tiles(const AttnArgs& a, const Entry& e, int rt, int group) {
+  const int r0 = rt * ROWS;
+  if (r0 >= e.n * group) return 0;
+  // a unit without keys still writes its zeros: one empty tile
+  return max(1, tile_list<kManyKeys, TREE>(a, e, r0 / group, min(e.n - 1, (r0 + ROWS - 1) / group)).count);
+}
+
+// Where tile `want` of a head's list lies: unit (entry e, its u-th row tile), the
+// list's tiles before that unit.  With want < 0: only `total`, the list's
+// length.  The wave goes through the list 64 units at a time: row tiles of
+// one entry, or entries of a row tile count, whichever is fewer steps.
+struct Place {
+  int e, u;
+  int64_t before, total;
+};
+
+template <int ROWS, bool TREE>
+__device__ __forceinline__ Place find_place(const AttnArgs& a, int64_t want) {
+  const int lane = (int)__lane_id(), group = a.heads_q / a.heads_kv;
+  const int most = (a.max_q * group + ROWS - 1) / ROWS;
+  Place p{0, 0, 0, 0};
+  if ((int64_t)a.entries * ((most + 63) / 64) <= (int64_t)((a.entries + 63) / 64) * most) {
+    for (int e = 0; e < a.entries; ++e) {
+      const Entry en = uniform(load_entry(a, e));
+      const int rts = row_tiles_of<ROWS>(en, group);
+      for (int b = 0; b < rts; b += 64) {
+        const int mine = b + lane < rts ? unit_tiles<ROWS, TREE>(a, en, row_tile_at(b + lane, rts), group) : 0;
+        const int upto = wave_scan_add(mine);
+        const uint64_t hit = __ballot(want >= 0 && p.total + upto > want);
+        if (hit) {
+          const int at = __builtin_ctzll(hit);
+          p.e = e;
+          p.u = b + at;
+          p.before = p.total + __shfl(upto - mine, at);
+          return p;
+        }
+        p.total += __shfl(upto, 63);
+      }
+    }
+    return p;
+  }
+  for (int b = 0; b < a.entries; b += 64) {
+    Entry en{};
+    if (b + lane < a.entries) en = load_entry(a, b + lane);
+    const int rts = row_tiles_of<ROWS>(en, group);
+    int mine = 0;
+    for (int rt = 0; rt < rts; ++rt) mine += unit_tiles<ROWS, TREE>(a, en, rt, group);
+    const int upto = wave_scan_add(mine);
+    const uint64_t hit = __ballot(want >= 0 && p.total + upto > want);
+    if (hit) {
+      const int at = __builtin_ctzll(hit);
+      p.e = b + at;
+      p.before = p.total + __shfl(upto - mine, at);
+      const Entry one = uniform(load_entry(a, p.e));
+      for (; p.u < row_tiles_of<ROWS>(one, group); ++p.u) {
+        const int n = unit_tiles<ROWS, TREE>(a, one, row_tile_at(p.u, row_tiles_of<ROWS>(one, group)), group);
+        if (p.before + n > want) break;
+        p.before += n;
+      }
+      return p;
+    }
+    p.total += __shfl(upto, 63);
+  }
+  return p;
+}
+
 template <typename T, int D, bool TREE>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_many_kernel(AttnArgs a) {
-  constexpr int STEPS = D / 16, DT = D / 32, KT = kManyKeys;
+__global__ __launch_bounds__(Many<D>::kThreads) void attention_many_kernel(AttnArgs a) {
+  constexpr int STEPS = D / 16, DT = D / 32, KT = kManyKeys, WAVES = Many<D>::kWaves, THREADS = Many<D>::kThreads;
+  constexpr int ROWS = Many<D>::kRows;
   constexpr int GRAN = KT * D / 8;                           // granules of one operand's tile
-  constexpr int PER = GRAN / kThreads;
+  constexpr int PER = GRAN / THREADS;
   extern __shared__ __align__(16) u32x4v lds[];              // [2][keys, values][GRAN]
   __shared__ int s_bad[2];
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, col = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int split = blockIdx.x % a.splits, rt = gridDim.x / a.splits - 1 - blockIdx.x / a.splits;
-  const int h = blockIdx.y, group = a.heads_q / a.heads_kv;
-  const Entry e = uniform(load_entry(a, blockIdx.z));
-  const int rows = e.n * group, r0 = rt * kManyRows;
-  if (r0 >= rows) return;
-  const int i0 = r0 / group, i1 = min(e.n - 1, (r0 + kManyRows - 1) / group);
-  const TileList list = tile_list<KT, TREE>(a, e, i0, i1);
-  const int chunk = (list.count + a.splits - 1) / a.splits;
-  const int t0 = split * chunk, t1 = min(list.count, t0 + chunk);
+  const int h = blockIdx.x % a.heads_kv, w = blockIdx.x / a.heads_kv, group = a.heads_q / a.heads_kv;
   const int P = 1 << a.page_log2, pmask = P - 1;
-
-  const int row = r0 + wave * 32 + col;
-  const bool live = row < rows;
-  const int i = live ? row / group : 0, hq = h * group + (live ? row % group : 0);
-  const RowMask mask = row_mask<TREE>(a, e, i, live);
-  const OpenKeys seen_by_all = open_keys<TREE>(a, e, i0, i1);
-  const bool wave_live = r0 + wave * 32 < rows;              // else it only carries tiles
-  u32x4v q[STEPS];
-  {
-    const uint16_t* src = a.q + (int64_t)(e.first + i) * a.q_stride + (int64_t)hq * D + half * 8;
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) q[s] = *reinterpret_cast<const u32x4v*>(src + s * 16);
-  }
-  f32x16 o[DT];
-#pragma unroll
-  for (int t = 0; t < DT; ++t) o[t] = f32x16{};
-  Running st{-INFINITY, 0.0f};
   const float c = a.scale * kLog2e;
 
-  u32x4v in[PER];                                            // a thread's granules of one operand on their way
-  // The page of each of a tile's keys, one key a lane.
-  auto pages_of = [&](int t) {
-    const int key = list.key<KT>(min(t, t1 - 1)) + lane;
-    return e.pages[min(key >> a.page_log2, (int)a.width - 1)];
-  };
-  const uint32_t page_elems = (uint32_t)(a.heads_kv * D) << a.page_log2, head_at = (uint32_t)(h * D) << a.page_log2;
-  // keys: granule g of the tile is dimension block g / 64 of key g % 64, so
-  // a thread keeps its key
-  auto fetch_keys = [&](int t, int32_t pk) {
-    const uint16_t* kp = a.k + (uint64_t)page_in_pool(pk, a.pages) * page_elems + head_at +
-                         (((list.key<KT>(t) + lane) & pmask) + wave * P) * 8;
-#pragma unroll
-    for (int n = 0; n < PER; ++n) in[n] = *reinterpret_cast<const u32x4v*>(kp + n * kWaves * P * 8);
-  };
-  // values: granule g is token block g / D of dimension g % D, one token
-  // block a wave, whose address the lane of the block's first key works out
-  auto fetch_values = [&](int t, int32_t pk) {
-    const uint64_t block = (uint64_t)(a.v + (uint64_t)page_in_pool(pk, a.pages) * page_elems + head_at +
-                                      (((list.key<KT>(t) + lane) & pmask) >> 3) * D * 8);
-#pragma unroll
-    for (int n = 0; n < PER; ++n) {
-      const int g = n * kThreads + wave * 64, at = g / D * 8;
-      const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)block, at);
-      const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(block >> 32), at);
-      in[n] = reinterpret_cast<const __attribute__((address_space(1))) u32x4v*>(((uint64_t)hi << 32) | lo)[g % D + lane];
+  int64_t run, left;                                         // tiles of a run, and of this one that are to come
+  Place at;
+  {
+    const int64_t total = uniform(find_place<ROWS, TREE>(a, -1).total);
+    run = max((total + a.target - 1) / a.target, (int64_t)kManyRun);
+    if (w * run >= total) {
+      if (h == 0 && tid == 0) a.part_note[w] = PartNote{0, 0, 0, 0};
+      return;
     }
-  };
-  auto store_keys = [&](int buf) {
-#pragma unroll
-    for (int n = 0; n < PER; ++n) lds[buf * 2 * GRAN + n * kThreads + tid] = in[n];
-  };
-  // s_bad: the last tile whose values had to be cleaned
-  auto store_values = [&](int buf, int t) {
-    if (!seen_by_all.tile(list.key<KT>(t), KT)) {
-      bool bad = false;
-#pragma unroll
-      for (int n = 0; n < PER; ++n) bad |= drop_nonfinite<T>(in[n]);
-      if (bad) s_bad[buf] = t;
-    }
-#pragma unroll
-    for (int n = 0; n < PER; ++n) lds[(buf * 2 + 1) * GRAN + n * kThreads + tid] = in[n];
-  };
-  auto rescale = [&](float alpha) {
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) o[d][r] *= alpha;
-  };
-
-  if (tid < 2) s_bad[tid] = -1;
-  lds_barrier();
-  int32_t page = 0;
-  if (t0 < t1) {
-    page = pages_of(t0);
-    fetch_keys(t0, page);
-    store_keys(0);
-    fetch_values(t0, page);
-    page = pages_of(t0 + 1);
-    store_values(0, t0);
+    left = min(run, total - w * run);
+    at = find_place<ROWS, TREE>(a, w * run);
+    at.before = w * run - at.before;                         // tiles of the first unit that lie in earlier runs
   }
-  lds_barrier();
-  const int krow = tile_key_of_row(col);
-  waitcnt_vm<0>();         // q has arrived: waits inside the loop are for the tiles' loads only
-  for (int t = t0; t < t1; ++t) {
-    const int buf = (t - t0) & 1, kb = list.key<KT>(t);
-    const bool more = t + 1 < t1;
-    const u32x4v* kt = lds + buf * 2 * GRAN + half * KT + krow;        // [2 s + half][32 x + key]
-    const u32x4v* vt = lds + (buf * 2 + 1) * GRAN + half * D + col;    // [4 x + 2 s + half][dimension]
-    if (more) fetch_keys(t + 1, page);
-    const bool open = seen_by_all.tile(kb, KT);
-    uint64_t seen = 0;
-    f32x16 s0[1] = {f32x16{}}, s1[1] = {f32x16{}};
-    u32x4v p0[2], p1[2];
-    float alpha;
-    bool moved = false;
-    if (wave_live) {
+  int first = (int)uniform(at.before), u = __builtin_amdgcn_readfirstlane(at.u);
+  int ei = __builtin_amdgcn_readfirstlane(at.e);
+  Entry e = uniform(load_entry(a, ei));
+  for (int segment = 0; left > 0; segment = 1, first = 0) {
+    while (u >= row_tiles_of<ROWS>(e, group)) {
+      u = 0;
+      if (++ei >= a.entries) return;                         // the lengths were changed under the call
+      e = uniform(load_entry(a, ei));
+    }
+    const int rt = row_tile_at(u++, row_tiles_of<ROWS>(e, group));
+    const int rows = e.n * group, r0 = rt * ROWS;
+    const int i0 = r0 / group, i1 = min(e.n - 1, (r0 + ROWS - 1) / group);
+    const TileList list = tile_list<KT, TREE>(a, e, i0, i1);
+    const int64_t rest = max(1, list.count) - first;         // of this unit
+    const bool whole = first == 0 && rest <= left;
+    const int t0 = first, t1 = min((int64_t)list.count, first + min(rest, left));
+    // for the fold: this run begins a unit and leaves it to others (its last segment)
+    if (h == 0 && tid == 0 && rest >= left)
+      a.part_note[w] = first == 0 && rest > left ? PartNote{(int)((rest - left + run - 1) / run) + 1, e.first, e.n * group, rt << 1 | segment}
+                                                 : PartNote{0, 0, 0, 0};
+    left -= min(rest, left);
+
+    const int row = r0 + wave * 32 + col;
+    RowMask mask;
+    // What all rows of the workgroup see (their values need no cleaning), what
+    // all rows of the wave see, and what any row of the wave sees: a wave
+    // only carries tiles outside that.
+    const OpenKeys seen_by_all = open_keys<TREE>(a, e, i0, i1);
+    const int w0 = r0 + wave * 32, j0 = min(w0, rows - 1) / group, j1 = min(w0 + 31, rows - 1) / group;
+    const OpenKeys seen_by_wave = open_keys<TREE>(a, e, j0, j1);
+    const OpenKeys reach = reach_keys<TREE>(a, e, j0, j1);
+    u32x4v q[STEPS];
+    {
+      const bool live = row < rows;
+      const int i = live ? row / group : 0, hq = h * group + (live ? row % group : 0);
+      mask = row_mask<TREE>(a, e, i, live);
+      const uint16_t* src = a.q + (int64_t)(e.first + i) * a.q_stride + (int64_t)hq * D + half * 8;
 #pragma unroll
-      for (int s = 0; s < STEPS; ++s) s0[0] = T::mfma(kt[2 * s * KT], q[s], s0[0]);
-      if (!open) {
-        seen = mask.bits<TREE>(kb);
-        cut_scores(s0[0], (uint32_t)seen);
+      for (int s = 0; s < STEPS; ++s) q[s] = *reinterpret_cast<const u32x4v*>(src + s * 16);
+    }
+    f32x16 o[DT];
+#pragma unroll
+    for (int t = 0; t < DT; ++t) o[t] = f32x16{};
+    Running st{-INFINITY, 0.0f};
+
+    // A thread's granules of the next tile on their way.  Both operands are
+    // under way for a whole tile where the registers allow it; at D = 256 they
+    // take turns in one set, half a tile each.
+    constexpr bool TURNS = D == 256;
+    u32x4v in[PER], in_v[TURNS ? 1 : PER];
+    // The page of each of a tile's keys, one key a lane.
+    auto pages_of = [&](int t) {
+      const int key = list.key<KT>(min(t, t1 - 1)) + lane;
+      return e.pages[min(key >> a.page_log2, (int)a.width - 1)];
+    };
+    const uint32_t page_elems = (uint32_t)(a.heads_kv * D) << a.page_log2, head_at = (uint32_t)(h * D) << a.page_log2;
+    // keys: granule g of the tile is dimension block g / 64 of key g % 64, so
+    // a thread keeps its key
+    auto fetch_keys = [&](int t, int32_t pk, u32x4v (&in)[PER]) {
+      const uint16_t* kp = a.k + (uint64_t)page_in_pool(pk, a.pages) * page_elems + head_at +
+                           (((list.key<KT>(t) + lane) & pmask) + wave * P) * 8;
+#pragma unroll
+      for (int n = 0; n < PER; ++n) in[n] = *reinterpret_cast<const u32x4v*>(kp + n * WAVES * P * 8);
+    };
+    // values: granule g is token block g / D of dimension g % D, one token
+    // block a wave, whose address the lane of the block's first key works out
+    auto fetch_values = [&](int t, int32_t pk, u32x4v (&in)[PER]) {
+      const uint64_t block = (uint64_t)(a.v + (uint64_t)page_in_pool(pk, a.pages) * page_elems + head_at +
+                                        (((list.key<KT>(t) + lane) & pmask) >> 3) * D * 8);
+#pragma unroll
+      for (int n = 0; n < PER; ++n) {
+        const int g = n * THREADS + wave * 64, from = g / D * 8;
+        const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)block, from);
+        const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(block >> 32), from);
+        const auto rsrc =
+            __builtin_amdgcn_make_buffer_rsrc((void*)(((uint64_t)hi << 32) | lo), 0, D * 16, kRawBufferWord3);
+        in[n] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, lane * 16, g % D * 16, 0);
       }
-      if (move_bound(s0, c, st, alpha)) rescale(alpha);
+    };
+    auto store_keys = [&](int buf, const u32x4v (&in)[PER]) {
 #pragma unroll
-      for (int s = 0; s < STEPS; ++s) s1[0] = T::mfma(kt[2 * s * KT + 32], q[s], s1[0]);
-      weigh(s0, c, st);
-      pack_weights<T>(s0[0], p0);
-      interleave<STEPS, 56 / STEPS, 16 / STEPS>();
-    }
-    if (more) {
-      store_keys(buf ^ 1);
-      fetch_values(t + 1, page);
-      page = pages_of(t + 2);
-    }
-    if (wave_live) {
-      if (!open) cut_scores(s1[0], (uint32_t)(seen >> 32));
-      moved = move_bound(s1, c, st, alpha);
+      for (int n = 0; n < PER; ++n) lds[buf * 2 * GRAN + n * THREADS + tid] = in[n];
+    };
+    // s_bad: the last tile whose values had to be cleaned
+    auto store_values = [&](int buf, int t, u32x4v (&in)[PER]) {
+      if (!seen_by_all.tile(list.key<KT>(t), KT)) {
+        bool bad = false;
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+        for (int n = 0; n < PER; ++n) bad |= drop_nonfinite<T>(in[n]);
+        if (bad) s_bad[buf] = t;
+      }
 #pragma unroll
-        for (int d = 0; d < DT; ++d) o[d] = T::mfma(vt[2 * s * D + d * 32], p0[s], o[d]);
-      weigh(s1, c, st);
-      pack_weights<T>(s1[0], p1);
-      interleave<2 * DT, 56 / (2 * DT), 16 / (2 * DT)>();
-      if (moved) rescale(alpha);                             // the first block was weighed with the earlier bound
+      for (int n = 0; n < PER; ++n) lds[(buf * 2 + 1) * GRAN + n * THREADS + tid] = in[n];
+    };
+    // At D = 256 the outputs stay in accumulation registers; left alone, the
+    // allocator copies all of them to vector registers and back in every tile.
+    auto settle = [&]() {
+      if constexpr (D == 256) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+        for (int d = 0; d < DT; ++d) asm volatile("" : "+a"(o[d]));
+      }
+    };
+    auto rescale = [&](float alpha) {
+      settle();
 #pragma unroll
-        for (int d = 0; d < DT; ++d) o[d] = T::mfma(vt[(4 + 2 * s) * D + d * 32], p1[s], o[d]);
-      if (!open && s_bad[buf] == t)
-        add_nonfinite<T, D, TREE>(a.v + head_at, e.pages, a.pages, page_elems, a.page_log2, mask, kb, KT, o);
-    }
-    if (more) store_values(buf ^ 1, t + 1);
-    lds_barrier();
-  }
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[d][r] *= alpha;
+      settle();
+    };
 
-  const float l = st.l + __shfl_xor(st.l, 32);
-  if (!live) return;
-  if (a.splits == 1) {
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    uint16_t* dst = a.out + ((int64_t)(e.first + i) * a.heads_q + hq) * D + 4 * half;
+    if (tid < 2) s_bad[tid] = -1;
+    lds_barrier();
+    int32_t page = 0;
+    if (t0 < t1) {
+      u32x4v too[PER];
+      page = pages_of(t0);
+      fetch_keys(t0, page, in);
+      fetch_values(t0, page, too);
+      page = pages_of(t0 + 1);
+      store_keys(0, in);
+      store_values(0, t0, too);
+    }
+    lds_barrier();
+    const int krow = tile_key_of_row(col);
+    waitcnt_vm<0>();         // q has arrived: waits inside the loop are for the tiles' loads only
+    for (int t = t0; t < t1; ++t) {
+      const int buf = (t - t0) & 1, kb = list.key<KT>(t);
+      const bool more = t + 1 < t1;
+      const u32x4v* kt = lds + buf * 2 * GRAN + half * KT + krow;        // [2 s + half][32 x + key]
+      const u32x4v* vt = lds + (buf * 2 + 1) * GRAN + half * D + col;    // [4 x + 2 s + half][dimension]
+      if (more) {
+        fetch_keys(t + 1, page, in);
+        if constexpr (!TURNS) {
+          fetch_values(t + 1, page, in_v);
+          page = pages_of(t + 2);
+        }
+      }
+      const bool open = seen_by_wave.tile(kb, KT);
+      const bool wave_live = w0 < rows && reach.touches(kb, KT);
+      uint64_t seen = 0;
+      f32x16 s0 = f32x16{}, s1 = f32x16{};
+      u32x4v p0[2], p1[2];
+      if (wave_live) {
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) s0 = T::mfma(kt[2 * s * KT], q[s], s0);
+        interleave<STEPS, 0, 0>();
+        if (!open) {
+          seen = mask.template bits<TREE>(kb);
+          cut_scores(s0, (uint32_t)seen);
+        }
+        float top = row_top(s0, c);
+        if (must_move(top, st)) rescale(move_bound(top, st));
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) s1 = T::mfma(kt[2 * s * KT + 32], q[s], s1);
+        float sum = weigh<T>(s0, c, st, p0);
+        interleave<STEPS, 56 / STEPS, 16 / STEPS>();
+        keep_here(p0, sum);
+        st.l += sum;
+      }
+      if constexpr (TURNS) {
+        if (more) {
+          store_keys(buf ^ 1, in);
+          fetch_values(t + 1, page, in);
+          page = pages_of(t + 2);
+        }
+      }
+      if (wave_live) {
+        if (!open) cut_scores(s1, (uint32_t)(seen >> 32));
+        float top = row_top(s1, c), alpha = 1.0f;
+        const bool moved = must_move(top, st);
+        if (moved) alpha = move_bound(top, st);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int d = 0; d < DT; ++d) o[d] = T::mfma(vt[2 * s * D + d * 32], p0[s], o[d]);
+        float sum = weigh<T>(s1, c, st, p1);
+        interleave<2 * DT, 56 / (2 * DT), 16 / (2 * DT)>();
+        keep_here(p1, sum);
+        if (moved) rescale(alpha);                           // the first block was weighed with the earlier bound
+        st.l += sum;
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int d = 0; d < DT; ++d) o[d] = T::mfma(vt[(4 + 2 * s) * D + d * 32], p1[s], o[d]);
+        interleave<2 * DT, 0, 0>();
+        settle();
+        if (s_bad[buf] == t) {
+          add_nonfinite<T, D, TREE>(a.v + head_at, e.pages, a.pages, page_elems, a.page_log2, mask, kb, KT, o);
+          settle();
+        }
+      }
+      if (more) {
+        if constexpr (TURNS) {
+          store_values(buf ^ 1, t + 1, in);
+        } else {
+          store_keys(buf ^ 1, in);
+          store_values(buf ^ 1, t + 1, in_v);
+        }
+      }
+      lds_barrier();
+    }
+
+    settle();
+    const float l = st.l + __shfl_xor(st.l, 32);
+    int local = wave * 32 + col;
+    asm volatile("" : "+v"(local));          // the row's numbers are worked out again, not kept through the loop
+    if (r0 + local >= rows) continue;
+    if (whole) {
+      const int i = (r0 + local) / group, hq = h * group + (r0 + local) % group;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      uint16_t* dst = a.out + ((int64_t)(e.first + i) * a.heads_q + hq) * D + 4 * half;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<u32x2v*>(dst + d * 32 + 8 * j) =
+              u32x2v{T::pack(o[d][4 * j] * inv, o[d][4 * j + 1] * inv), T::pack(o[d][4 * j + 2] * inv, o[d][4 * j + 3] * inv)};
+      continue;
+    }
+    const int64_t slot = ((int64_t)blockIdx.x * 2 + segment) * ROWS + local;
+    if (half == 0) *reinterpret_cast<f32x2p*>(a.part_ml + slot * 2) = f32x2p{st.m, l};
+    if (st.m == -INFINITY) continue;
+    float* part = a.part_o + slot * D + 4 * half;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<u32x2v*>(dst + d * 32 + 8 * j) =
-            u32x2v{T::pack(o[d][4 * j] * inv, o[d][4 * j + 1] * inv), T::pack(o[d][4 * j + 2] * inv, o[d][4 * j + 3] * inv)};
-    return;
+        *reinterpret_cast<f32x4v*>(part + d * 32 + 8 * j) =
+            f32x4v{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
   }
-  const int64_t at = ((int64_t)(e.first + i) * a.heads_q + hq) * a.splits + split;
-  if (half == 0) *reinterpret_cast<f32x2p*>(a.part_ml + at * 2) = f32x2p{st.m, l};
-  if (st.m == -INFINITY) return;
-  float* part = a.part_o + at * D + 4 * half;
-#pragma unroll
-  for (int d = 0; d < DT; ++d)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<f32x4v*>(part + d * 32 + 8 * j) =
-          f32x4v{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
 }
 
 // ---- fold ----------------------------------------------------------------
-// o = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s, one wave per output row.
-template <typename T, int D, bool TREE, bool FEW>
-__global__ __launch_bounds__(64) void attention_fold_kernel(AttnArgs a) {
-  constexpr int V = D / 64;
-  const int lane = threadIdx.x;
-  int64_t ml, step;                                          // first (m, l) pair, distance between parts
-  int splits;
-  int64_t out_row;
-  if (FEW) {
-    const Unit u = find_unit<TREE>(a, blockIdx.z, true);
-    if (!u.live || u.splits == 1) return;
-    const Entry e = load_entry(a, u.e);
-    const int h = blockIdx.y, group = a.heads_q / a.heads_kv, row = blockIdx.x;
-    if (row >= e.n * group) return;
-    splits = u.splits;
-    ml = ((int64_t)u.base * a.heads_kv + h) * kFewRows + row;
-    step = (int64_t)a.heads_kv * kFewRows;
-    out_row = (int64_t)(e.first + row / group) * a.heads_q + h * group + row % group;
-  } else {
-    const Entry e = load_entry(a, blockIdx.z);
-    if ((int)blockIdx.x >= e.n) return;
-    splits = a.splits;
-    out_row = (int64_t)(e.first + blockIdx.x) * a.heads_q + blockIdx.y;
-    ml = out_row * splits;
-    step = 1;
-  }
+// o = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s over the parts s of a row.
+
+// 256 threads take 1024 / D rows of a unit, four dimensions each; the note of
+// the unit's first part says how many there are.
+//   few-row kernel:  parts are slots blockIdx.x, + 1, ...; a slot holds 32 rows a head
+//   many-row kernel: the first part is in place 0 or 1 of run blockIdx.x's slot,
+//                    the others in place 0 of the runs after it
+template <typename T, int D, bool FEW>
+__global__ __launch_bounds__(kThreads) void attention_fold_kernel(AttnArgs a) {
+  constexpr int LANES = D / 4, ROWS = kThreads / LANES, SLOT = FEW ? kFewRows : Many<D>::kRows;
+  const PartNote note = a.part_note[blockIdx.x];
+  if (note.parts == 0) return;
+  const int local = blockIdx.y * ROWS + threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
+  const int h = blockIdx.z, group = a.heads_q / a.heads_kv;
+  const int row = FEW ? local : (note.place >> 1) * SLOT + local;
+  if (row >= note.rows) return;
+  auto slot = [&](int s) -> int64_t {
+    const int64_t at = (int64_t)(blockIdx.x + s) * a.heads_kv + h;
+    return (FEW ? at : at * 2 + (s ? 0 : note.place & 1)) * SLOT + local;
+  };
+  // the row's D / 4 lanes read its (m, l) pairs side by side
+  const int gl = threadIdx.x % LANES;
   float top = -INFINITY;
-  for (int s = lane; s < splits; s += 64) top = fmaxf(top, a.part_ml[(ml + s * step) * 2]);
+  for (int s = gl; s < note.parts; s += LANES) top = fmaxf(top, a.part_ml[slot(s) * 2]);
 #pragma unroll
-  for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-  float acc[V] = {}, sum = 0.0f;
+  for (int x = LANES / 2; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
+  f32x4v acc = {};
+  float sum = 0.0f;
   if (top != -INFINITY) {
-    for (int s = 0; s < splits; ++s) {
-      const float m = a.part_ml[(ml + s * step) * 2], l = a.part_ml[(ml + s * step) * 2 + 1];
-      if (m == -INFINITY) continue;
-      const float f = __builtin_amdgcn_exp2f(m - top);
-      sum += f * l;
-      const float* src = a.part_o + (ml + s * step) * D + lane * V;
+    for (int base = 0; base < note.parts; base += LANES) {
+      float f = 0.0f;
+      if (base + gl < note.parts) {
+        const f32x2p ml = *reinterpret_cast<const f32x2p*>(a.part_ml + slot(base + gl) * 2);
+        f = ml[0] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml[0] - top);
+        sum += f * ml[1];
+      }
+      const int n = min(LANES, note.parts - base);
+#pragma unroll 8
+      for (int s = 0; s < n; ++s) {
+        const float fs = __shfl(f, s, LANES);
+        const f32x4v x = *reinterpret_cast<const f32x4v*>(a.part_o + slot(base + s) * D + d);
+        // a part that saw no key left its outputs unwritten
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] += f * src[v];
+        for (int v = 0; v < 4; ++v) acc[v] += fs != 0.0f ? fs * x[v] : 0.0f;
+      }
     }
+#pragma unroll
+    for (int x = LANES / 2; x; x >>= 1) sum += __shfl_xor(sum, x);
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  uint16_t* dst = a.out + out_row * D + lane * V;
-#pragma unroll
-  for (int v = 0; v < V; ++v) dst[v] = (uint16_t)T::pack(acc[v] * inv, 0.0f);
+  uint16_t* dst = a.out + ((int64_t)(note.first + row / group) * a.heads_q + h * group + row % group) * D + d;
+  *reinterpret_cast<u32x2v*>(dst) = u32x2v{T::pack(acc[0] * inv, acc[1] * inv), T::pack(acc[2] * inv, acc[3] * inv)};
 }
 
 bool few_rows(const AttnArgs& a) { return (int64_t)a.max_q * (a.heads_q / a.heads_kv) <= kFewRows; }
@@ -458,56 +645,43 @@ int few_target(const AttnArgs& a) {
 }
 int64_t few_slots(const AttnArgs& a) { return (int64_t)few_target(a) + a.entries; }
 
-int64_t row_tiles(const AttnArgs& a) {
-  return ((int64_t)a.max_q * (a.heads_q / a.heads_kv) + kManyRows - 1) / kManyRows;
+// Runs per key head of the many-row kernel: its resident workgroups over the heads.
+int many_target(const AttnArgs& a) {
+  const int resident = device_cus() * (a.head_dim == 64 ? 2 : 1);
+  return resident / a.heads_kv > 1 ? resident / a.heads_kv : 1;
 }
-
-// Parts of every unit's keys in the many-row kernel: enough that the grid
-// holds two workgroups a compute unit, none shorter than four tiles.
-int many_splits(const AttnArgs& a) {
-  const int64_t units = row_tiles(a) * a.heads_kv * a.entries;
-  int64_t s = 2 * (int64_t)device_cus() / (units > 0 ? units : 1);
-  int64_t keys = a.width << a.page_log2;
-  const int64_t reach = (int64_t)a.window + a.max_q + a.sinks;
-  if (a.window > 0 && reach < keys) keys = reach;
-  const int64_t most = keys / (4 * kManyKeys);
-  if (s > most) s = most;
-  return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
-}
-
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
-// (partial outputs, (m, l) pairs) in bytes
-void part_bytes(const AttnArgs& a, size_t* o, size_t* ml) {
-  int64_t rows;
-  if (few_rows(a)) {
-    rows = few_slots(a) * a.heads_kv * kFewRows;
-  } else {
-    const int s = many_splits(a);
-    rows = s == 1 ? 0 : a.tokens * a.heads_q * s;
-  }
-  *o = round256((size_t)rows * a.head_dim * 4);
-  *ml = round256((size_t)rows * 8);
+// The workspace: partial outputs, (m, l) pairs, notes.
+struct Parts {
+  size_t o, ml, notes;
+};
+
+Parts part_bytes(const AttnArgs& a) {
+  const int64_t slots = few_rows(a) ? few_slots(a) : many_target(a);
+  const int64_t rows = slots * a.heads_kv * (few_rows(a) ? kFewRows : 2 * (a.head_dim == 256 ? Many<256>::kRows : Many<128>::kRows));
+  return {round256((size_t)rows * a.head_dim * 4), round256((size_t)rows * 8), round256((size_t)slots * sizeof(PartNote))};
 }
 
 template <typename T, int D, bool TREE>
 hipError_t launch_typed(AttnArgs& a, hipStream_t stream) {
+  constexpr int FOLD = kThreads * 4 / D;                     // rows of a fold workgroup
   if (few_rows(a)) {
     a.target = few_target(a);
-    attention_few_kernel<T, D, TREE><<<dim3((unsigned)few_slots(a), a.heads_kv), kThreads, 0, stream>>>(a);
-    attention_fold_kernel<T, D, TREE, true>
-        <<<dim3(a.max_q * (a.heads_q / a.heads_kv), a.heads_kv, a.entries), 64, 0, stream>>>(a);
+    const unsigned slots = (unsigned)few_slots(a), rows = (unsigned)(a.max_q * (a.heads_q / a.heads_kv));
+    attention_few_kernel<T, D, TREE><<<dim3(slots, a.heads_kv), kThreads, 0, stream>>>(a);
+    attention_fold_kernel<T, D, true>
+        <<<dim3(slots, (rows + FOLD - 1) / FOLD, a.heads_kv), kThreads, 0, stream>>>(a);
     return hipGetLastError();
   }
   constexpr size_t lds = 2 * 2 * (size_t)kManyKeys * D * 2;
   static hipError_t ready = hipFuncSetAttribute((const void*)&attention_many_kernel<T, D, TREE>,
                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (ready != hipSuccess) return ready;
-  a.splits = many_splits(a);
-  attention_many_kernel<T, D, TREE>
-      <<<dim3((unsigned)(row_tiles(a) * a.splits), a.heads_kv, a.entries), kThreads, lds, stream>>>(a);
-  if (a.splits > 1)
-    attention_fold_kernel<T, D, TREE, false><<<dim3(a.max_q, a.heads_q, a.entries), 64, 0, stream>>>(a);
+  a.target = many_target(a);
+  attention_many_kernel<T, D, TREE><<<(unsigned)(a.target * a.heads_kv), Many<D>::kThreads, lds, stream>>>(a);
+  attention_fold_kernel<T, D, false>
+      <<<dim3((unsigned)a.target, Many<D>::kRows / FOLD, a.heads_kv), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -528,16 +702,16 @@ hipError_t launch_dim(AttnArgs& a, hipStream_t stream) {
 }  // namespace
 
 size_t attention_workspace_bytes(const AttnArgs& a) {
-  size_t o, ml;
-  part_bytes(a, &o, &ml);
-  return o + ml;
+  const Parts p = part_bytes(a);
+  return p.o + p.ml + p.notes;
 }
 
 hipError_t launch_attention(AttnArgs a, void* workspace, hipStream_t stream) {
-  size_t o, ml;
-  part_bytes(a, &o, &ml);
-  a.part_o = reinterpret_cast<float*>(workspace);
-  a.part_ml = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + o);
+  const Parts p = part_bytes(a);
+  char* w = reinterpret_cast<char*>(workspace);
+  a.part_o = reinterpret_cast<float*>(w);
+  a.part_ml = reinterpret_cast<float*>(w + p.o);
+  a.part_note = reinterpret_cast<PartNote*>(w + p.o + p.ml);
   return a.fp16 ? launch_dim<F16>(a, stream) : launch_dim<Bf16>(a, stream);
 }
 

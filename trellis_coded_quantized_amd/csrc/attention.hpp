@@ -64,16 +64,19 @@ __device__ __forceinline__ Entry load_entry(const AttnArgs& a, int e) {
   return r;
 }
 
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uint64_t)v);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)((uint64_t)v >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
 // The same entry with its numbers in scalar registers (all lanes hold the same).
 __device__ __forceinline__ Entry uniform(Entry e) {
   e.first = __builtin_amdgcn_readfirstlane(e.first);
   e.n = __builtin_amdgcn_readfirstlane(e.n);
   e.ctx = __builtin_amdgcn_readfirstlane(e.ctx);
   e.total = __builtin_amdgcn_readfirstlane(e.total);
-  const uint64_t p = (uint64_t)e.pages;
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32));
-  e.pages = (GlobalInts)(((uint64_t)hi << 32) | lo);
+  e.pages = (GlobalInts)uniform((int64_t)e.pages);
   return e;
 }
 
@@ -166,12 +169,22 @@ struct OpenKeys {
   __device__ __forceinline__ bool tile(int kb, int keys) const {
     return kb + keys <= to && (kb >= from || kb + keys <= sinks);
   }
+  __device__ __forceinline__ bool touches(int kb, int keys) const {
+    return kb < to && (kb + keys > from || kb < sinks);
+  }
 };
 
 template <bool TREE>
 __device__ __forceinline__ OpenKeys open_keys(const AttnArgs& a, const Entry& e, int i0, int i1) {
   if (TREE) return {0, e.ctx, 0};
   return {a.window > 0 ? max(e.ctx + i1 - a.window + 1, 0) : 0, min(e.ctx + i0 + 1, e.total), a.sinks};
+}
+
+// The keys that any row of tokens i0 .. i1 may see.
+template <bool TREE>
+__device__ __forceinline__ OpenKeys reach_keys(const AttnArgs& a, const Entry& e, int i0, int i1) {
+  if (TREE) return {0, e.total, 0};
+  return {a.window > 0 ? max(e.ctx + i0 - a.window + 1, 0) : 0, min(e.ctx + i1 + 1, e.total), a.sinks};
 }
 
 // x and the same of the lane 32 away, the larger of the two.
@@ -187,47 +200,48 @@ struct Running {
   float l;     // sum of weights over this lane's keys
 };
 
-// Move the running bound to the scores of NS 32-key tiles.  Returns whether any
-// row of the wave moved; `alpha` is then what the lane's earlier sums (done
-// here) and outputs have to be multiplied with.
-template <int NS>
-__device__ __forceinline__ bool move_bound(const f32x16 (&s)[NS], float c, Running& st, float& alpha) {
-  float top = s[0][0];
+// The largest score of a row over a 32-key tile, scaled.
+__device__ __forceinline__ float row_top(const f32x16& s, float c) {
+  float top = s[0];
 #pragma unroll
-  for (int t = 0; t < NS; ++t)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) top = fmaxf(top, s[t][r]);
-  top = max_of_halves(top) * c;
-  if (!__any(top > st.m + kRescaleStep)) return false;   // -inf + 8 = -inf: a first visible key moves it
-  const float m = fmaxf(st.m, top);
-  alpha = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.m - m);
-  st.m = m;
-  st.l *= alpha;
-  return true;
+  for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
+  return max_of_halves(top) * c;
 }
 
-// Scores -> weights in place (unrounded), added to the lane's sum.
-template <int NS>
-__device__ __forceinline__ void weigh(f32x16 (&s)[NS], float c, Running& st) {
+// Whether any row of the wave has to move its bound for that score (-inf + 8
+// = -inf: a first visible key moves it).
+__device__ __forceinline__ bool must_move(float top, const Running& st) {
+  return __any(top > st.m + kRescaleStep);
+}
+
+// Moves the bound; returns what the lane's earlier sum (done here) and outputs
+// have to be multiplied with.
+__device__ __forceinline__ float move_bound(float top, Running& st) {
+  const float m = fmaxf(st.m, top);
+  const float alpha = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.m - m);
+  st.m = m;
+  st.l *= alpha;
+  return alpha;
+}
+
+// Scores -> weights under the current bound, rounded and packed as the B
+// operands of the second product; returns their unrounded sum over this
+// lane's keys.
+template <typename T>
+__device__ __forceinline__ float weigh(const f32x16& s, float c, const Running& st, u32x4v (&p)[2]) {
   const float bound = st.m == -INFINITY ? 0.0f : st.m;
   float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-  for (int t = 0; t < NS; ++t)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      s[t][r] = __builtin_amdgcn_exp2f(fmaf(s[t][r], c, -bound));
-      sum[r & 1] += s[t][r];
-    }
-  st.l += sum[0] + sum[1];
-}
-
-// The B operands of the second product: weights of one tile, rounded.
-template <typename T>
-__device__ __forceinline__ void pack_weights(const f32x16& s, u32x4v (&p)[2]) {
-#pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int w = 0; w < 4; ++w) p[h][w] = T::pack(s[8 * h + 2 * w], s[8 * h + 2 * w + 1]);
+    for (int w = 0; w < 4; ++w) {
+      const float x = __builtin_amdgcn_exp2f(fmaf(s[8 * h + 2 * w], c, -bound));
+      const float y = __builtin_amdgcn_exp2f(fmaf(s[8 * h + 2 * w + 1], c, -bound));
+      sum[0] += x;
+      sum[1] += y;
+      p[h][w] = T::pack(x, y);
+    }
+  return sum[0] + sum[1];
 }
 
 // Zero weights do not hide an infinity or NaN among the values (0 * inf =

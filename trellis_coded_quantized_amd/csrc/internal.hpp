@@ -83,6 +83,13 @@ int api_fail(int code, const char* fmt, ...);
 int api_ok();
 int api_hip(const char* fn, hipError_t e);
 
+// What the fold of split keys has to know of a unit, written by its first part.
+struct PartNote {
+  int parts;                  // 0: nothing to fold here
+  int first, rows;            // the entry's first row of q, its rows per key head
+  int place;                  // many-row kernel: row tile << 1 | place of the first part
+};
+
 // One attention call.  TREE: `ancestors` is set, window and sinks are 0.
 struct AttnArgs {
   const uint16_t* q;
@@ -96,12 +103,12 @@ struct AttnArgs {
   uint16_t* out;
   float* part_o;              // partial outputs of split entries
   float* part_ml;             // their (bound, sum) pairs
+  PartNote* part_note;
   int64_t tokens, q_stride, width, seqs;
   uint32_t pages;
   int entries, max_q, heads_q, heads_kv, head_dim, page_log2;
   int window, sinks, fp16;
-  int target;                 // few-row kernel: workgroups wanted per key head
-  int splits;                 // many-row kernel: parts of every unit's keys
+  int target;                 // workgroups per key head that the keys are cut for
   float scale;
 };
 
