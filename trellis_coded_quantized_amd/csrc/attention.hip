@@ -65,8 +65,9 @@ __device__ __forceinline__ Unit find_unit(const AttnArgs& a, int slot) {
 template <typename T, int D, bool TREE>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_few_kernel(AttnArgs a) {
   constexpr int STEPS = D / 16, DT = D / 32;
+  constexpr int JOIN = DT < 4 ? DT : 4;                      // 32-dimension tiles joined at a time
   __shared__ float s_m[kWaves][32], s_l[kWaves][32];
-  __shared__ __align__(16) float s_o[kWaves][32][36];
+  __shared__ __align__(16) float s_o[kWaves][32][JOIN * 32 + 4];
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, col = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = blockIdx.y, group = a.heads_q / a.heads_kv;
@@ -80,62 +81,92 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_few_kern
   const TileList list = tile_list<32, TREE>(a, e, 0, e.n - 1);
   const int t0 = u.split * u.chunk, t1 = min(list.count, t0 + u.chunk);
   const int P = 1 << a.page_log2, pmask = P - 1;
+  const uint32_t page_elems = (uint32_t)(a.heads_kv * D) << a.page_log2, head_at = (uint32_t)(h * D) << a.page_log2;
+  const int krow = tile_key_of_row(col);
+
+  // A wave takes every fourth tile.  Keys of the next one are under way while
+  // the softmax and the second product of this one run, values while the next
+  // one's scores are computed; page numbers are a tile further ahead.
+  u32x4v kf[STEPS], vf[2][DT];
+  int page[2];                                               // of a tile's two halves of 16 keys
+  auto load_pages = [&](int t) {
+    const int kb = list.key<32>(min(t, t1 - 1));
+    page[0] = e.pages[min(kb >> a.page_log2, (int)a.width - 1)];
+    page[1] = e.pages[min((kb + 16) >> a.page_log2, (int)a.width - 1)];
+  };
+  uint64_t at[2];                                            // their elements in the pools
+  auto locate = [&]() {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      at[s] = (uint64_t)page_in_pool(__builtin_amdgcn_readfirstlane(page[s]), a.pages) * page_elems + head_at;
+  };
+  auto load_keys = [&](int t) {
+    const int kb = list.key<32>(t);
+    const uint16_t* kp = a.k + (krow >= 16 ? at[1] : at[0]) + (((kb + krow) & pmask) + half * P) * 8;
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) kf[s] = *reinterpret_cast<const u32x4v*>(kp + s * 16 * P);
+  };
+  auto load_values = [&](int t) {
+    const int kb = list.key<32>(t);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const uint16_t* vp = a.v + at[s] + (((kb + s * 16) & pmask) >> 3) * D * 8;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+        vf[s][d] = *reinterpret_cast<const u32x4v*>(vp + (uint32_t)((half * D + col) * 8 + d * 256));
+    }
+  };
+  int t = t0 + wave;
+  if (t < t1) load_pages(t);
 
   const bool live = col < rows;
   const int i = live ? col / group : 0, hq = h * group + (live ? col % group : 0);
-  const RowMask mask = row_mask<TREE>(a, e, i, live);
-  const OpenKeys seen_by_all = open_keys<TREE>(a, e, 0, e.n - 1);
   u32x4v q[STEPS];
   {
     const uint16_t* src = a.q + (int64_t)(e.first + i) * a.q_stride + (int64_t)hq * D + half * 8;
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) q[s] = *reinterpret_cast<const u32x4v*>(src + s * 16);
   }
+  const RowMask mask = row_mask<TREE>(a, e, i, live);
+  const OpenKeys seen_by_all = open_keys<TREE>(a, e, 0, e.n - 1);
+  if (t < t1) {
+    locate();
+    load_keys(t);
+    load_values(t);
+    load_pages(t + kWaves);
+  }
 
   f32x16 o[DT];
 #pragma unroll
-  for (int t = 0; t < DT; ++t) o[t] = f32x16{};
+  for (int d = 0; d < DT; ++d) o[d] = f32x16{};
   Running st{-INFINITY, 0.0f};
   const float c = a.scale * kLog2e;
-  const int64_t head_elems = (int64_t)D << a.page_log2;      // one head's page
-  const int krow = tile_key_of_row(col);
-
-  for (int t = t0 + wave; t < t1; t += kWaves) {
+  for (; t < t1; t += kWaves) {
     const int kb = list.key<32>(t);
-    const int p0 = kb >> a.page_log2, p1 = (kb + 16) >> a.page_log2;
-    const int64_t g0 = ((int64_t)page_in_pool(e.pages[min(p0, (int)a.width - 1)], a.pages) * a.heads_kv + h) * head_elems;
-    const int64_t g1 = ((int64_t)page_in_pool(e.pages[min(p1, (int)a.width - 1)], a.pages) * a.heads_kv + h) * head_elems;
-    const uint16_t* kp = a.k + (krow >= 16 ? g1 : g0) + (((kb + krow) & pmask) + half * P) * 8;
-    u32x4v kf[STEPS];
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) kf[s] = *reinterpret_cast<const u32x4v*>(kp + (int64_t)s * 16 * P);
-    u32x4v vf[2][DT];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int key = kb + s * 16 + half * 8;
-      const uint16_t* vp = a.v + (s ? g1 : g0) + (int64_t)((key & pmask) >> 3) * D * 8 + col * 8;
-#pragma unroll
-      for (int d = 0; d < DT; ++d) vf[s][d] = *reinterpret_cast<const u32x4v*>(vp + d * 256);
-    }
+    const bool more = t + kWaves < t1;
     f32x16 sc = f32x16{};
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) sc = T::mfma(kf[s], q[s], sc);
-    const bool open = seen_by_all.tile(kb, 32);
+    if (more) {
+      locate();
+      load_keys(t + kWaves);
+      load_pages(t + 2 * kWaves);
+    }
     bool bad = false;
-    if (!open) {
+    if (!seen_by_all.tile(kb, 32)) {
       cut_scores(sc, (uint32_t)mask.bits<TREE>(kb));
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int d = 0; d < DT; ++d) bad |= drop_nonfinite<T>(vf[s][d]);
+      bad = drop_nonfinite<T>(vf[0]);
+      bad |= drop_nonfinite<T>(vf[1]);
     }
     const float top = row_top(sc, c);
     if (must_move(top, st)) {
       const float alpha = move_bound(top, st);
+      settle(o);
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[d][r] *= alpha;
+      settle(o);
     }
     u32x4v p[2];
     st.l += weigh<T>(sc, c, st, p);
@@ -143,10 +174,14 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_few_kern
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int s = 0; s < 2; ++s) o[d] = T::mfma(vf[s][d], p[s], o[d]);
-    if (__any(bad))
-      add_nonfinite<T, D, TREE>(a.v + h * head_elems, e.pages, a.pages, (uint32_t)(a.heads_kv * head_elems),
-                                a.page_log2, mask, kb, 32, o);
+    if (more) load_values(t + kWaves);
+    settle(o);
+    if (__any(bad)) {
+      add_nonfinite<T, D, TREE>(a.v + head_at, e.pages, a.pages, page_elems, a.page_log2, mask, kb, 32, o);
+      settle(o);
+    }
   }
+  settle(o);
 
   // join the four waves
   st.l += __shfl_xor(st.l, 32);
@@ -173,23 +208,29 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_few_kern
   uint16_t* dst = a.out + ((int64_t)(e.first + orow / group) * a.heads_q + h * group + orow % group) * D + od;
   float* part = a.part_o + (slot * kFewRows + orow) * D + od;
 #pragma unroll
-  for (int d = 0; d < DT; ++d) {
+  for (int d0 = 0; d0 < DT; d0 += JOIN) {
+    if (d0) __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<f32x4v*>(&s_o[wave][col][8 * j + 4 * half]) =
-          f32x4v{o[d][4 * j] * f, o[d][4 * j + 1] * f, o[d][4 * j + 2] * f, o[d][4 * j + 3] * f};
+    for (int d = 0; d < JOIN; ++d)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f32x16& x = o[d0 + d];
+        *reinterpret_cast<f32x4v*>(&s_o[wave][col][d * 32 + 8 * j + 4 * half]) =
+            f32x4v{x[4 * j] * f, x[4 * j + 1] * f, x[4 * j + 2] * f, x[4 * j + 3] * f};
+      }
     __syncthreads();
-    f32x4v sum = *reinterpret_cast<const f32x4v*>(&s_o[0][orow][od]);
+    if (!owrite) continue;
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) sum += *reinterpret_cast<const f32x4v*>(&s_o[w][orow][od]);
-    if (owrite) {
+    for (int d = 0; d < JOIN; ++d) {
+      f32x4v sum = *reinterpret_cast<const f32x4v*>(&s_o[0][orow][d * 32 + od]);
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) sum += *reinterpret_cast<const f32x4v*>(&s_o[w][orow][d * 32 + od]);
       if (whole)
-        *reinterpret_cast<u32x2v*>(dst + d * 32) =
+        *reinterpret_cast<u32x2v*>(dst + (d0 + d) * 32) =
             u32x2v{T::pack(sum[0] * inv, sum[1] * inv), T::pack(sum[2] * inv, sum[3] * inv)};
       else
-        *reinterpret_cast<f32x4v*>(part + d * 32) = sum;
+        *reinterpret_cast<f32x4v*>(part + (d0 + d) * 32) = sum;
     }
-    __syncthreads();
   }
   if (!whole && owrite && (tid & 7) == 0)
     *reinterpret_cast<f32x2p*>(a.part_ml + (slot * kFewRows + orow) * 2) = f32x2p{otop, osum};
@@ -433,29 +474,18 @@ __global__ __launch_bounds__(Many<D>::kThreads) void attention_many_kernel(AttnA
     // s_bad: the last tile whose values had to be cleaned
     auto store_values = [&](int buf, int t, u32x4v (&in)[PER]) {
       if (!seen_by_all.tile(list.key<KT>(t), KT)) {
-        bool bad = false;
-#pragma unroll
-        for (int n = 0; n < PER; ++n) bad |= drop_nonfinite<T>(in[n]);
-        if (bad) s_bad[buf] = t;
+        if (drop_nonfinite<T>(in)) s_bad[buf] = t;
       }
 #pragma unroll
       for (int n = 0; n < PER; ++n) lds[(buf * 2 + 1) * GRAN + n * THREADS + tid] = in[n];
     };
-    // At D = 256 the outputs stay in accumulation registers; left alone, the
-    // allocator copies all of them to vector registers and back in every tile.
-    auto settle = [&]() {
-      if constexpr (D == 256) {
-#pragma unroll
-        for (int d = 0; d < DT; ++d) asm volatile("" : "+a"(o[d]));
-      }
-    };
     auto rescale = [&](float alpha) {
-      settle();
+      settle(o);
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[d][r] *= alpha;
-      settle();
+      settle(o);
     };
 
     if (tid < 2) s_bad[tid] = -1;
@@ -533,10 +563,10 @@ __global__ __launch_bounds__(Many<D>::kThreads) void attention_many_kernel(AttnA
 #pragma unroll
           for (int d = 0; d < DT; ++d) o[d] = T::mfma(vt[(4 + 2 * s) * D + d * 32], p1[s], o[d]);
         interleave<2 * DT, 0, 0>();
-        settle();
+        settle(o);
         if (s_bad[buf] == t) {
           add_nonfinite<T, D, TREE>(a.v + head_at, e.pages, a.pages, page_elems, a.page_log2, mask, kb, KT, o);
-          settle();
+          settle(o);
         }
       }
       if (more) {
@@ -550,7 +580,7 @@ __global__ __launch_bounds__(Many<D>::kThreads) void attention_many_kernel(AttnA
       lds_barrier();
     }
 
-    settle();
+    settle(o);
     const float l = st.l + __shfl_xor(st.l, 32);
     int local = wave * 32 + col;
     asm volatile("" : "+v"(local));          // the row's numbers are worked out again, not kept through the loop

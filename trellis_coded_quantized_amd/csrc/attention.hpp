@@ -244,23 +244,40 @@ __device__ __forceinline__ float weigh(const f32x16& s, float c, const Running& 
   return sum[0] + sum[1];
 }
 
+// At D = 256 a wave's outputs stay in accumulation registers; left alone, the
+// allocator copies all of them to vector registers and back in every tile.
+template <int DT>
+__device__ __forceinline__ void settle(f32x16 (&o)[DT]) {
+  if constexpr (DT == 8) {
+#pragma unroll
+    for (int d = 0; d < DT; ++d) asm volatile("" : "+a"(o[d]));
+  }
+}
+
 // Zero weights do not hide an infinity or NaN among the values (0 * inf =
 // NaN), and such values may stand where a row does not look, or where nothing
 // was ever written.  In a tile that some row sees in part they therefore
 // enter the product as zeros (drop_nonfinite, which says whether there were
 // any), and rows that do see one get it back from here: each lane walks the
 // tile's keys and adds what its row sees to its own outputs.
-template <typename T>
-__device__ __forceinline__ bool drop_nonfinite(u32x4v& v) {
-  bool any = false;
+template <typename T, int N>
+__device__ __forceinline__ bool drop_nonfinite(u32x4v (&v)[N]) {
+  // an exponent of all ones carries into the sign's place when its last bit is added
+  constexpr uint32_t E = T::kExp * 0x10001u, L = (T::kExp & (0u - T::kExp)) * 0x10001u;
+  uint32_t any = 0;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const uint32_t x = v[w];
-    const bool lo = (x & T::kExp) == T::kExp, hi = (x & (T::kExp << 16)) == (T::kExp << 16);
-    v[w] = (lo ? 0u : x & 0xFFFFu) | (hi ? 0u : x & 0xFFFF0000u);
-    any |= lo || hi;
-  }
-  return any;
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) any |= (v[n][w] & E) + L;
+  if (!__any((any & 0x80008000u) != 0)) return false;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t x = v[n][w], hit = ((x & E) + L) & 0x80008000u;
+      v[n][w] = x & ~((hit >> 15) * 0xFFFFu);
+    }
+  return (any & 0x80008000u) != 0;
 }
 
 template <typename T, int D, bool TREE>
