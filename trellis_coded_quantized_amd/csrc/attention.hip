@@ -23,6 +23,7 @@ constexpr int kManyRun = 4;               // fewest tiles that it cuts the keys 
 
 struct Unit {
   int e, split, splits, chunk;
+  int own_base, own_splits;               // the slots of entry number `slot`, whose note this workgroup writes
   bool live;
 };
 
@@ -34,7 +35,7 @@ __device__ __forceinline__ int entry_tiles(const AttnArgs& a, int e) {
   return max(1, tile_list<32, TREE>(a, en, 0, en.n - 1).count);
 }
 
-// Slot -> (entry, split).
+// Slot -> (entry, split); slot numbers reach past the entries' numbers.
 template <bool TREE>
 __device__ __forceinline__ Unit find_unit(const AttnArgs& a, int slot) {
   const int lane = (int)__lane_id();
@@ -49,15 +50,19 @@ __device__ __forceinline__ Unit find_unit(const AttnArgs& a, int slot) {
     const int parts = (tiles + u.chunk - 1) / u.chunk;
     const int upto = wave_scan_add(parts);
     const uint64_t hit = __ballot(before + upto > slot);
-    if (hit) {
+    if (hit && !u.live) {
       const int at = __builtin_ctzll(hit);
       u.e = b + at;
-      u.splits = __builtin_amdgcn_readfirstlane(__shfl(parts, at));
-      u.split = slot - before - __builtin_amdgcn_readfirstlane(__shfl(upto, at)) + u.splits;
+      u.splits = __builtin_amdgcn_readlane(parts, at);
+      u.split = slot - before - __builtin_amdgcn_readlane(upto, at) + u.splits;
       u.live = true;
-      return u;
     }
-    before += __builtin_amdgcn_readfirstlane(__shfl(upto, 63));
+    if (slot >= b && slot < b + 64) {
+      u.own_splits = __builtin_amdgcn_readlane(parts, slot - b);
+      u.own_base = before + __builtin_amdgcn_readlane(upto, slot - b) - u.own_splits;
+    }
+    if (u.live && slot < b + 64) break;
+    before += __builtin_amdgcn_readlane(upto, 63);
   }
   return u;
 }
@@ -72,12 +77,18 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_few_kern
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = blockIdx.y, group = a.heads_q / a.heads_kv;
   const Unit u = find_unit<TREE>(a, blockIdx.x);
-  const Entry e = u.live ? uniform(load_entry(a, u.e)) : Entry{};
-  const int rows = e.n * group;
-  if (h == 0 && tid == 0)                                    // for the fold: a split unit's first slot says so
-    a.part_note[blockIdx.x] = u.live && u.split == 0 && u.splits > 1 ? PartNote{u.splits, e.first, rows, 0}
-                                                                     : PartNote{0, 0, 0, 0};
+  if (h == 0 && tid == 0 && (int)blockIdx.x < a.entries) {   // for the fold
+    PartNote note{u.own_splits > 1 ? u.own_splits : 0, 0, 0, u.own_base};
+    if (note.parts) {
+      const Entry own = load_entry(a, blockIdx.x);
+      note.first = own.first;
+      note.rows = own.n * group;
+    }
+    a.part_note[blockIdx.x] = note;
+  }
   if (!u.live) return;
+  const Entry e = uniform(load_entry(a, u.e));
+  const int rows = e.n * group;
   const TileList list = tile_list<32, TREE>(a, e, 0, e.n - 1);
   const int t0 = u.split * u.chunk, t1 = min(list.count, t0 + u.chunk);
   const int P = 1 << a.page_log2, pmask = P - 1;
@@ -613,26 +624,27 @@ __global__ __launch_bounds__(Many<D>::kThreads) void attention_many_kernel(AttnA
 // ---- fold ----------------------------------------------------------------
 // o = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s over the parts s of a row.
 
-// 256 threads take 1024 / D rows of a unit, four dimensions each; the note of
-// the unit's first part says how many there are.
-//   few-row kernel:  parts are slots blockIdx.x, + 1, ...; a slot holds 32 rows a head
-//   many-row kernel: the first part is in place 0 or 1 of run blockIdx.x's slot,
-//                    the others in place 0 of the runs after it
+// D / 4 lanes take a row's dimensions, and read its (m, l) pairs side by side.
+// The note of the unit says where its parts are.
+//   few-row kernel:  notes by entry; parts are consecutive slots of 32 rows a head.
+//     One row a workgroup, its 1024 / D groups of lanes take the parts in turn.
+//   many-row kernel: notes by the run that begins the unit; the first part is
+//     in place 0 or 1 of that run's slot, the others in place 0 of the runs
+//     after it.  1024 / D rows a workgroup.
 template <typename T, int D, bool FEW>
 __global__ __launch_bounds__(kThreads) void attention_fold_kernel(AttnArgs a) {
-  constexpr int LANES = D / 4, ROWS = kThreads / LANES, SLOT = FEW ? kFewRows : Many<D>::kRows;
+  constexpr int LANES = D / 4, GROUPS = kThreads / LANES, SLOT = FEW ? kFewRows : Many<D>::kRows, BATCH = 8;
   const PartNote note = a.part_note[blockIdx.x];
   if (note.parts == 0) return;
-  const int local = blockIdx.y * ROWS + threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
+  const int gl = threadIdx.x % LANES, g = threadIdx.x / LANES, d = gl * 4;
   const int h = blockIdx.z, group = a.heads_q / a.heads_kv;
+  const int local = FEW ? blockIdx.y : blockIdx.y * GROUPS + g;
   const int row = FEW ? local : (note.place >> 1) * SLOT + local;
-  if (row >= note.rows) return;
+  if (row >= note.rows) return;                              // FEW: the whole workgroup
   auto slot = [&](int s) -> int64_t {
-    const int64_t at = (int64_t)(blockIdx.x + s) * a.heads_kv + h;
+    const int64_t at = (int64_t)((FEW ? note.place : (int)blockIdx.x) + s) * a.heads_kv + h;
     return (FEW ? at : at * 2 + (s ? 0 : note.place & 1)) * SLOT + local;
   };
-  // the row's D / 4 lanes read its (m, l) pairs side by side
-  const int gl = threadIdx.x % LANES;
   float top = -INFINITY;
   for (int s = gl; s < note.parts; s += LANES) top = fmaxf(top, a.part_ml[slot(s) * 2]);
 #pragma unroll
@@ -648,17 +660,29 @@ __global__ __launch_bounds__(kThreads) void attention_fold_kernel(AttnArgs a) {
         sum += f * ml[1];
       }
       const int n = min(LANES, note.parts - base);
-#pragma unroll 8
-      for (int s = 0; s < n; ++s) {
-        const float fs = __shfl(f, s, LANES);
-        const f32x4v x = *reinterpret_cast<const f32x4v*>(a.part_o + slot(base + s) * D + d);
-        // a part that saw no key left its outputs unwritten
+      for (int s0 = FEW ? g * BATCH : 0; s0 < n; s0 += FEW ? GROUPS * BATCH : BATCH) {
+        f32x4v x[BATCH];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) acc[v] += fs != 0.0f ? fs * x[v] : 0.0f;
+        for (int k = 0; k < BATCH; ++k)
+          x[k] = *reinterpret_cast<const f32x4v*>(a.part_o + slot(base + min(s0 + k, n - 1)) * D + d);
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+          const float fs = s0 + k < n ? __shfl(f, (s0 + k) % LANES, LANES) : 0.0f;
+          // a part that saw no key left its outputs unwritten
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[v] += fs != 0.0f ? fs * x[k][v] : 0.0f;
+        }
       }
     }
 #pragma unroll
     for (int x = LANES / 2; x; x >>= 1) sum += __shfl_xor(sum, x);
+  }
+  if (FEW) {
+    __shared__ f32x4v s_acc[kThreads];
+    s_acc[threadIdx.x] = acc;
+    __syncthreads();
+    if (g) return;
+    for (int o = 1; o < GROUPS; ++o) acc += s_acc[o * LANES + gl];
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   uint16_t* dst = a.out + ((int64_t)(note.first + row / group) * a.heads_q + h * group + row % group) * D + d;
@@ -695,13 +719,11 @@ Parts part_bytes(const AttnArgs& a) {
 
 template <typename T, int D, bool TREE>
 hipError_t launch_typed(AttnArgs& a, hipStream_t stream) {
-  constexpr int FOLD = kThreads * 4 / D;                     // rows of a fold workgroup
   if (few_rows(a)) {
     a.target = few_target(a);
     const unsigned slots = (unsigned)few_slots(a), rows = (unsigned)(a.max_q * (a.heads_q / a.heads_kv));
     attention_few_kernel<T, D, TREE><<<dim3(slots, a.heads_kv), kThreads, 0, stream>>>(a);
-    attention_fold_kernel<T, D, true>
-        <<<dim3(slots, (rows + FOLD - 1) / FOLD, a.heads_kv), kThreads, 0, stream>>>(a);
+    attention_fold_kernel<T, D, true><<<dim3(a.entries, rows, a.heads_kv), kThreads, 0, stream>>>(a);
     return hipGetLastError();
   }
   constexpr size_t lds = 2 * 2 * (size_t)kManyKeys * D * 2;
@@ -711,7 +733,7 @@ hipError_t launch_typed(AttnArgs& a, hipStream_t stream) {
   a.target = many_target(a);
   attention_many_kernel<T, D, TREE><<<(unsigned)(a.target * a.heads_kv), Many<D>::kThreads, lds, stream>>>(a);
   attention_fold_kernel<T, D, false>
-      <<<dim3((unsigned)a.target, Many<D>::kRows / FOLD, a.heads_kv), kThreads, 0, stream>>>(a);
+      <<<dim3((unsigned)a.target, Many<D>::kRows * D / (4 * kThreads), a.heads_kv), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 

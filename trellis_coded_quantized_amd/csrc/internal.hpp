@@ -83,11 +83,11 @@ int api_fail(int code, const char* fmt, ...);
 int api_ok();
 int api_hip(const char* fn, hipError_t e);
 
-// What the fold of split keys has to know of a unit, written by its first part.
+// What the fold of split keys has to know of a unit.
 struct PartNote {
   int parts;                  // 0: nothing to fold here
   int first, rows;            // the entry's first row of q, its rows per key head
-  int place;                  // many-row kernel: row tile << 1 | place of the first part
+  int place;                  // few rows: slot of the first part; many: row tile << 1 | place of the first part
 };
 
 // One attention call.  TREE: `ancestors` is set, window and sinks are 0.
