@@ -123,6 +123,7 @@ int attention_sizes(const char* fn, const trellis_kv_cache* cache, const trellis
   a->heads_kv = cache->heads;
   a->head_dim = cache->head_dim;
   a->page_log2 = log2_of(cache->page_size);
+  a->tree = tree;
   a->window = window;
   const int64_t room = state->width * cache->page_size;
   a->sinks = (int64_t)sinks < room ? sinks : (int)room;

@@ -13,13 +13,86 @@ constexpr int kFewRows = 32;              // rows of the few-row kernel: one MFM
 constexpr int kManyKeys = 64;             // keys of a tile of the many-row kernel
 constexpr int kManyRun = 4;               // fewest tiles that it cuts the keys into
 
+// ---- cutting keys --------------------------------------------------------
+// Units of work (all rows of an entry, or a tile of them) whose keys are cut
+// into chunks of equally many tiles, so that the slots (unit, chunk) fill the
+// `target` workgroups of a key head.  Every workgroup works the same cut out
+// from the lengths, 64 entries at a time, one a lane.
+constexpr int kRounds = 3;                // slots per workgroup where entries are many and unlike
+
+struct Cut {
+  int tiles, units;                       // this lane's entry of the first 64
+  int chunk;
+};
+
+__device__ __forceinline__ int64_t wave_sum64(int64_t v) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
+// sizes(e, tiles, units): how long the units of entry e are and how many.
+// One slot a workgroup if a chunk little longer than the mean does it (the
+// chunk grows until its slots fit), else kRounds of a third.  In the end all
+// slots fit, or no unit is cut.
+template <typename Sizes>
+__device__ __forceinline__ Cut find_cut(const AttnArgs& a, int least, const Sizes& sizes) {
+  const int lane = (int)__lane_id();
+  Cut cut{0, 0, 0};
+  if (lane < a.entries) sizes(lane, cut.tiles, cut.units);
+  int64_t total = (int64_t)cut.tiles * cut.units;
+  int longest = cut.tiles;
+  for (int b = 64; b < a.entries; b += 64) {
+    int t = 0, n = 0;
+    if (b + lane < a.entries) sizes(b + lane, t, n);
+    total += (int64_t)t * n;
+    longest = max(longest, t);
+  }
+  total = uniform(wave_sum64(total));
+#pragma unroll
+  for (int d = 32; d; d >>= 1) longest = max(longest, __shfl_xor(longest, d));
+  longest = __builtin_amdgcn_readfirstlane(longest);
+  auto slots = [&](int c) {
+    int64_t n = (int64_t)((cut.tiles + c - 1) / c) * cut.units;
+    for (int b = 64; b < a.entries; b += 64) {
+      int t = 0, u = 0;
+      if (b + lane < a.entries) sizes(b + lane, t, u);
+      n += (int64_t)((t + c - 1) / c) * u;
+    }
+    return uniform(wave_sum64(n));
+  };
+  for (int rounds = 1;; rounds = a.rounds) {
+    const int64_t room = (int64_t)rounds * a.target, mean = (total + room - 1) / room;
+    int64_t c = mean < least ? least : mean;
+    if (c >= longest) {
+      cut.chunk = __builtin_amdgcn_readfirstlane(max(longest, 1));
+      return cut;
+    }
+    if (a.entries == 1 && cut.units == 1) {                  // mean was rounded up: it fits
+      cut.chunk = __builtin_amdgcn_readfirstlane((int)c);
+      return cut;
+    }
+    bool fits = false;
+    for (int tries = 0; tries < 5 && c < longest; ++tries) {
+      const int64_t n = slots((int)c);
+      if (n <= room) {
+        fits = true;
+        break;
+      }
+      c = max(c + 1, c * n / room);
+    }
+    if (rounds == a.rounds || (fits && c * 4 <= mean * 5)) {
+      cut.chunk = __builtin_amdgcn_readfirstlane(fits ? (int)c : max(longest, 1));
+      return cut;
+    }
+  }
+}
+
 // ---- few rows ------------------------------------------------------------
 // All rows of an entry that share a key head (tokens x query heads per key
 // head, at most 32) are one MFMA tile, so keys and values are read once,
-// straight into operand registers.  The keys of all entries are cut into
-// chunks of `chunk` tiles, chosen from the sum of the entries' tiles so that
-// about `target` workgroups per key head have equal work however unlike the
-// lengths are.  Every workgroup computes the same cut from the lengths.
+// straight into operand registers; the four waves of a workgroup take the
+// tiles of its chunk in turn.
 
 struct Unit {
   int e, split, splits, chunk;
@@ -40,11 +113,12 @@ template <bool TREE>
 __device__ __forceinline__ Unit find_unit(const AttnArgs& a, int slot) {
   const int lane = (int)__lane_id();
   Unit u{};
-  int tiles = entry_tiles<TREE>(a, lane);
-  int total = wave_sum(tiles);
-  for (int b = 64; b < a.entries; b += 64) total += wave_sum(entry_tiles<TREE>(a, b + lane));
-  u.chunk = __builtin_amdgcn_readfirstlane(max(kWaves, (total + a.target - 1) / a.target));
-  int before = 0;
+  const Cut cut = find_cut(a, kWaves, [&](int e, int& tiles, int& units) {
+    tiles = entry_tiles<TREE>(a, e);
+    units = 1;
+  });
+  u.chunk = cut.chunk;
+  int before = 0, tiles = cut.tiles;
   for (int b = 0; b < a.entries; b += 64) {
     if (b) tiles = entry_tiles<TREE>(a, b + lane);
     const int parts = (tiles + u.chunk - 1) / u.chunk;
@@ -78,7 +152,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_few_kern
   const int h = blockIdx.y, group = a.heads_q / a.heads_kv;
   const Unit u = find_unit<TREE>(a, blockIdx.x);
   if (h == 0 && tid == 0 && (int)blockIdx.x < a.entries) {   // for the fold
-    PartNote note{u.own_splits > 1 ? u.own_splits : 0, 0, 0, u.own_base};
+    PartNote note{u.own_splits > 1 ? u.own_splits : 0, 0, 0, u.own_base, 1};
     if (note.parts) {
       const Entry own = load_entry(a, blockIdx.x);
       note.first = own.first;
@@ -87,10 +161,11 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_few_kern
     a.part_note[blockIdx.x] = note;
   }
   if (!u.live) return;
-  const Entry e = uniform(load_entry(a, u.e));
+  const Entry e = uniform(load_entry(a, __builtin_amdgcn_readfirstlane(u.e)));
   const int rows = e.n * group;
   const TileList list = tile_list<32, TREE>(a, e, 0, e.n - 1);
-  const int t0 = u.split * u.chunk, t1 = min(list.count, t0 + u.chunk);
+  const int t0 = __builtin_amdgcn_readfirstlane(u.split * u.chunk);
+  const int t1 = __builtin_amdgcn_readfirstlane(min(list.count, t0 + u.chunk));
   const int P = 1 << a.page_log2, pmask = P - 1;
   const uint32_t page_elems = (uint32_t)(a.heads_kv * D) << a.page_log2, head_at = (uint32_t)(h * D) << a.page_log2;
   const int krow = tile_key_of_row(col);
@@ -286,14 +361,22 @@ __device__ __forceinline__ void keep_here(u32x4v (&p)[2], float& sum) {
   asm volatile("" : "+v"(p[0]), "+v"(p[1]), "+v"(sum));
 }
 
-// The work of a key head is the list of its units (entry, row tile), tokens
-// ascending, each as long as the key tiles it reads.  Every workgroup takes an
-// equal run of that list, whatever the lengths and masks are: a run may end
-// inside a unit, and the unit then goes on in the next workgroup.  Parts of
-// units go to the workspace (a workgroup has at most two: the end of a unit it
-// did not begin, in place 0 of its slot, and the beginning of one it does not
-// end, in place 1) and are folded by the kernel after this one; whole units
-// are written by the workgroup that has them.
+// Which workgroup does what.  A unit is (entry, row tile).
+//
+// Consecutive tokens: units of a head form one list, each as long as the key
+// tiles it reads.  Every workgroup takes an equal run of that list, whatever
+// the lengths and masks are: a run may end inside a unit, and the unit then
+// goes on in the next workgroup.  Parts of units go to the workspace (a
+// workgroup has at most two: the end of a unit it did not begin, in place 0 of
+// its slot, and the beginning of one it does not end, in place 1).
+//
+// Trees: all row tiles of an entry read the same keys, far more of them than
+// the caches hold, so workgroups that share keys should read them at the same
+// time.  The units are cut into equal chunks of tiles, and slots run
+// (entry, chunk, row tile) with the row tiles innermost.
+//
+// Parts are folded by the kernel after this one; whole units are written by
+// the workgroup that has them.
 
 template <int ROWS>
 __device__ __forceinline__ int row_tiles_of(const Entry& e, int group) {
@@ -313,63 +396,136 @@ __device__ __forceinline__ int unit_tiles(const AttnArgs& a, const Entry& e, int
   return max(1, tile_list<kManyKeys, TREE>(a, e, r0 / group, min(e.n - 1, (r0 + ROWS - 1) / group)).count);
 }
 
-// Where tile `want` of a head's list lies: unit (entry e, its u-th row tile), the
-// list's tiles before that unit.  With want < 0: only `total`, the list's
-// length.  The wave goes through the list 64 units at a time: row tiles of
-// one entry, or entries of a row tile count, whichever is fewer steps.
+// Where the run of workgroup w begins: the u-th row tile of entry e, with
+// `first` of its tiles in earlier runs.  The wave goes through the list 64
+// units at a time: row tiles of one entry, or entries of a row tile count,
+// whichever is fewer steps; a list of one step is gone through once.
 struct Place {
   int e, u;
-  int64_t before, total;
+  int64_t first, run, left;               // left: tiles of the run, 0: none
 };
 
-template <int ROWS, bool TREE>
-__device__ __forceinline__ Place find_place(const AttnArgs& a, int64_t want) {
+template <int ROWS>
+__device__ __forceinline__ Place find_place(const AttnArgs& a, int w) {
   const int lane = (int)__lane_id(), group = a.heads_q / a.heads_kv;
   const int most = (a.max_q * group + ROWS - 1) / ROWS;
-  Place p{0, 0, 0, 0};
-  if ((int64_t)a.entries * ((most + 63) / 64) <= (int64_t)((a.entries + 63) / 64) * most) {
-    for (int e = 0; e < a.entries; ++e) {
-      const Entry en = uniform(load_entry(a, e));
+  const bool by_entry = (int64_t)((a.entries + 63) / 64) * most < (int64_t)a.entries * ((most + 63) / 64);
+  Place p{};
+  auto entry_sum = [&](int e) {
+    int n = 0;
+    if (e < a.entries) {
+      const Entry en = load_entry(a, e);
       const int rts = row_tiles_of<ROWS>(en, group);
-      for (int b = 0; b < rts; b += 64) {
-        const int mine = b + lane < rts ? unit_tiles<ROWS, TREE>(a, en, row_tile_at(b + lane, rts), group) : 0;
-        const int upto = wave_scan_add(mine);
-        const uint64_t hit = __ballot(want >= 0 && p.total + upto > want);
+      for (int rt = 0; rt < rts; ++rt) n += unit_tiles<ROWS, false>(a, en, rt, group);
+    }
+    return n;
+  };
+  auto unit_of = [&](const Entry& en, int u) {
+    const int rts = row_tiles_of<ROWS>(en, group);
+    return u < rts ? unit_tiles<ROWS, false>(a, en, row_tile_at(u, rts), group) : 0;
+  };
+  // the first step's lengths, and the length of the list
+  const Entry e0 = uniform(load_entry(a, 0));
+  const int mine0 = by_entry ? entry_sum(lane) : unit_of(e0, lane);
+  int64_t total = 0;
+  if (by_entry) {
+    total = mine0;
+    for (int b = 64; b < a.entries; b += 64) total += entry_sum(b + lane);
+  } else {
+    total = mine0;
+    for (int e = 0; e < a.entries; ++e) {
+      const Entry en = e ? uniform(load_entry(a, e)) : e0;
+      for (int b = e ? 0 : 64; b < row_tiles_of<ROWS>(en, group); b += 64) total += unit_of(en, b + lane);
+    }
+  }
+  total = uniform(wave_sum64(total));
+  p.run = max((total + a.target - 1) / a.target, (int64_t)kManyRun);
+  const int64_t want = w * p.run;
+  if (want >= total) return p;
+  p.left = min(p.run, total - want);
+  int64_t before = 0;
+  if (by_entry) {
+    for (int b = 0; b < a.entries; b += 64) {
+      const int mine = b ? entry_sum(b + lane) : mine0, upto = wave_scan_add(mine);
+      const uint64_t hit = __ballot(before + upto > want);
+      if (hit) {
+        const int at = __builtin_ctzll(hit);
+        p.e = b + at;
+        before += __builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(mine, at);
+        const Entry en = uniform(load_entry(a, p.e));
+        for (; p.u < row_tiles_of<ROWS>(en, group); ++p.u) {
+          const int n = unit_of(en, p.u);
+          if (before + n > want) break;
+          before += n;
+        }
+        break;
+      }
+      before += __builtin_amdgcn_readlane(upto, 63);
+    }
+  } else {
+    for (; p.e < a.entries; ++p.e) {
+      const Entry en = p.e ? uniform(load_entry(a, p.e)) : e0;
+      bool found = false;
+      for (int b = 0; b < row_tiles_of<ROWS>(en, group); b += 64) {
+        const int mine = p.e + b ? unit_of(en, b + lane) : mine0, upto = wave_scan_add(mine);
+        const uint64_t hit = __ballot(before + upto > want);
         if (hit) {
           const int at = __builtin_ctzll(hit);
-          p.e = e;
           p.u = b + at;
-          p.before = p.total + __shfl(upto - mine, at);
-          return p;
+          before += __builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(mine, at);
+          found = true;
+          break;
         }
-        p.total += __shfl(upto, 63);
+        before += __builtin_amdgcn_readlane(upto, 63);
       }
+      if (found) break;
     }
-    return p;
   }
+  p.first = want - before;
+  return p;
+}
+
+// Slot `slot` of a tree call: entry, row tile, and which of the chunks.
+struct Slot {
+  int e, rt, part, parts;
+  bool live;
+};
+
+template <int ROWS>
+__device__ __forceinline__ int tree_tiles(const AttnArgs& a, int e, int& units) {
+  const int group = a.heads_q / a.heads_kv;
+  units = 0;
+  if (e >= a.entries) return 0;
+  const Entry en = load_entry(a, e);
+  units = row_tiles_of<ROWS>(en, group);
+  return units ? unit_tiles<ROWS, true>(a, en, 0, group) : 0;
+}
+
+template <int ROWS>
+__device__ __forceinline__ Slot find_slot(const AttnArgs& a, const int (&tiles0)[64], const int (&units0)[64], int chunk,
+                                          int64_t slot) {
+  const int lane = (int)__lane_id();
+  Slot s{};
+  int64_t before = 0;
   for (int b = 0; b < a.entries; b += 64) {
-    Entry en{};
-    if (b + lane < a.entries) en = load_entry(a, b + lane);
-    const int rts = row_tiles_of<ROWS>(en, group);
-    int mine = 0;
-    for (int rt = 0; rt < rts; ++rt) mine += unit_tiles<ROWS, TREE>(a, en, rt, group);
-    const int upto = wave_scan_add(mine);
-    const uint64_t hit = __ballot(want >= 0 && p.total + upto > want);
+    int tiles = tiles0[lane], units = units0[lane];
+    if (b) tiles = tree_tiles<ROWS>(a, b + lane, units);
+    const int parts = (tiles + chunk - 1) / chunk, mine = parts * units, upto = wave_scan_add(mine);
+    const uint64_t hit = __ballot(before + upto > slot);
     if (hit) {
       const int at = __builtin_ctzll(hit);
-      p.e = b + at;
-      p.before = p.total + __shfl(upto - mine, at);
-      const Entry one = uniform(load_entry(a, p.e));
-      for (; p.u < row_tiles_of<ROWS>(one, group); ++p.u) {
-        const int n = unit_tiles<ROWS, TREE>(a, one, row_tile_at(p.u, row_tiles_of<ROWS>(one, group)), group);
-        if (p.before + n > want) break;
-        p.before += n;
-      }
-      return p;
+      const int in = (int)(slot - before) - __builtin_amdgcn_readlane(upto, at) + __builtin_amdgcn_readlane(mine, at);
+      const int rts = __builtin_amdgcn_readlane(units, at);
+      s.e = b + at;
+      s.parts = __builtin_amdgcn_readlane(parts, at);
+      s.part = __builtin_amdgcn_readfirstlane(in / rts);
+      s.rt = in - s.part * rts;
+      s.live = true;
+      return s;
     }
-    p.total += __shfl(upto, 63);
+    before += __builtin_amdgcn_readlane(upto, 63);
   }
-  return p;
+  return s;
 }
 
 template <typename T, int D, bool TREE>
@@ -386,40 +542,81 @@ __global__ __launch_bounds__(Many<D>::kThreads) void attention_many_kernel(AttnA
   const int P = 1 << a.page_log2, pmask = P - 1;
   const float c = a.scale * kLog2e;
 
-  int64_t run, left;                                         // tiles of a run, and of this one that are to come
-  Place at;
-  {
-    const int64_t total = uniform(find_place<ROWS, TREE>(a, -1).total);
-    run = max((total + a.target - 1) / a.target, (int64_t)kManyRun);
-    if (w * run >= total) {
-      if (h == 0 && tid == 0) a.part_note[w] = PartNote{0, 0, 0, 0};
+  __shared__ int s_tiles[64], s_units[64];                   // trees: the first entries, kept out of registers
+  int chunk = 1;
+  Place at{};                                                // consecutive tokens
+  Entry e{};
+  int ei = -1;
+  if constexpr (TREE) {
+    const Cut cut = find_cut(a, kManyRun, [&](int x, int& tiles, int& units) { tiles = tree_tiles<ROWS>(a, x, units); });
+    chunk = cut.chunk;
+    if (wave == 0) {
+      s_tiles[lane] = cut.tiles;
+      s_units[lane] = cut.units;
+    }
+    lds_barrier();
+  } else {
+    at = find_place<ROWS>(a, w);
+    at.first = uniform(at.first);
+    at.left = uniform(at.left);
+    at.e = __builtin_amdgcn_readfirstlane(at.e);
+    at.u = __builtin_amdgcn_readfirstlane(at.u);
+    if (at.left == 0) {
+      if (h == 0 && tid == 0) a.part_note[w] = PartNote{0, 0, 0, 0, 0};
       return;
     }
-    left = min(run, total - w * run);
-    at = find_place<ROWS, TREE>(a, w * run);
-    at.before = w * run - at.before;                         // tiles of the first unit that lie in earlier runs
   }
-  int first = (int)uniform(at.before), u = __builtin_amdgcn_readfirstlane(at.u);
-  int ei = __builtin_amdgcn_readfirstlane(at.e);
-  Entry e = uniform(load_entry(a, ei));
-  for (int segment = 0; left > 0; segment = 1, first = 0) {
-    while (u >= row_tiles_of<ROWS>(e, group)) {
-      u = 0;
-      if (++ei >= a.entries) return;                         // the lengths were changed under the call
+  for (int segment = 0;; ++segment) {
+    int rt, first;                                           // the unit, and its tiles before this segment
+    int64_t slot_at, upto;                                   // where a part goes, the tile that ends the segment
+    if constexpr (TREE) {
+      slot_at = w + (int64_t)segment * a.target;
+      const Slot s = find_slot<ROWS>(a, s_tiles, s_units, chunk, slot_at);
+      if (!s.live) {
+        // notes are read for as many slots as can hold parts
+        if (h == 0 && tid == 0 && segment < a.rounds) a.part_note[slot_at] = PartNote{0, 0, 0, 0, 0};
+        if (segment + 1 >= a.rounds) return;
+        continue;
+      }
+      ei = __builtin_amdgcn_readfirstlane(s.e);
+      rt = __builtin_amdgcn_readfirstlane(s.rt);
       e = uniform(load_entry(a, ei));
+      first = s.part * chunk;
+      upto = first + chunk;
+      if (h == 0 && tid == 0 && segment < a.rounds)
+        a.part_note[slot_at] = s.part == 0 && s.parts > 1
+                                   ? PartNote{s.parts, e.first, e.n * group, rt, row_tiles_of<ROWS>(e, group)}
+                                   : PartNote{0, 0, 0, 0, 0};
+    } else {
+      if (at.left <= 0) return;
+      if (ei < 0) e = uniform(load_entry(a, ei = at.e));
+      while (at.u >= row_tiles_of<ROWS>(e, group)) {
+        at.u = 0;
+        if (++ei >= a.entries) return;                       // the lengths were changed under the call
+        e = uniform(load_entry(a, ei));
+      }
+      rt = row_tile_at(at.u++, row_tiles_of<ROWS>(e, group));
+      first = (int)at.first;
+      at.first = 0;
+      upto = first + at.left;
+      slot_at = (int64_t)w * 2 + (segment != 0);
     }
-    const int rt = row_tile_at(u++, row_tiles_of<ROWS>(e, group));
     const int rows = e.n * group, r0 = rt * ROWS;
     const int i0 = r0 / group, i1 = min(e.n - 1, (r0 + ROWS - 1) / group);
     const TileList list = tile_list<KT, TREE>(a, e, i0, i1);
-    const int64_t rest = max(1, list.count) - first;         // of this unit
-    const bool whole = first == 0 && rest <= left;
-    const int t0 = first, t1 = min((int64_t)list.count, first + min(rest, left));
-    // for the fold: this run begins a unit and leaves it to others (its last segment)
-    if (h == 0 && tid == 0 && rest >= left)
-      a.part_note[w] = first == 0 && rest > left ? PartNote{(int)((rest - left + run - 1) / run) + 1, e.first, e.n * group, rt << 1 | segment}
-                                                 : PartNote{0, 0, 0, 0};
-    left -= min(rest, left);
+    const int count = max(1, list.count);
+    const bool whole = first == 0 && count <= upto;
+    const int t0 = __builtin_amdgcn_readfirstlane(first);
+    const int t1 = __builtin_amdgcn_readfirstlane((int)min((int64_t)list.count, upto));
+    if constexpr (!TREE) {
+      // this run begins a unit and leaves it to others (its last segment)
+      if (h == 0 && tid == 0 && count >= upto)
+        a.part_note[w] = first == 0 && count > upto
+                             ? PartNote{(int)((count - upto + at.run - 1) / at.run) + 1, e.first, e.n * group,
+                                        rt << 1 | (segment != 0), 0}
+                             : PartNote{0, 0, 0, 0, 0};
+      at.left -= min(upto, (int64_t)count) - first;
+    }
 
     const int row = r0 + wave * 32 + col;
     RowMask mask;
@@ -608,7 +805,7 @@ __global__ __launch_bounds__(Many<D>::kThreads) void attention_many_kernel(AttnA
               u32x2v{T::pack(o[d][4 * j] * inv, o[d][4 * j + 1] * inv), T::pack(o[d][4 * j + 2] * inv, o[d][4 * j + 3] * inv)};
       continue;
     }
-    const int64_t slot = ((int64_t)blockIdx.x * 2 + segment) * ROWS + local;
+    const int64_t slot = (slot_at * a.heads_kv + h) * ROWS + local;
     if (half == 0) *reinterpret_cast<f32x2p*>(a.part_ml + slot * 2) = f32x2p{st.m, l};
     if (st.m == -INFINITY) continue;
     float* part = a.part_o + slot * D + 4 * half;
@@ -626,24 +823,30 @@ __global__ __launch_bounds__(Many<D>::kThreads) void attention_many_kernel(AttnA
 
 // D / 4 lanes take a row's dimensions, and read its (m, l) pairs side by side.
 // The note of the unit says where its parts are.
-//   few-row kernel:  notes by entry; parts are consecutive slots of 32 rows a head.
+//   few rows:   notes by entry; parts are consecutive slots of 32 rows a head.
 //     One row a workgroup, its 1024 / D groups of lanes take the parts in turn.
-//   many-row kernel: notes by the run that begins the unit; the first part is
-//     in place 0 or 1 of that run's slot, the others in place 0 of the runs
-//     after it.  1024 / D rows a workgroup.
-template <typename T, int D, bool FEW>
+//   many rows, trees: notes by the slot of the first part, parts every `step` slots.
+//   many rows, consecutive tokens: notes by the run that begins the unit; the
+//     first part is in place 0 or 1 of that run, the others in place 0 of the
+//     runs after it.  1024 / D rows a workgroup for both.
+enum FoldKind { kFoldFew, kFoldTree, kFoldRuns };
+
+template <typename T, int D, FoldKind KIND>
 __global__ __launch_bounds__(kThreads) void attention_fold_kernel(AttnArgs a) {
+  constexpr bool FEW = KIND == kFoldFew;
   constexpr int LANES = D / 4, GROUPS = kThreads / LANES, SLOT = FEW ? kFewRows : Many<D>::kRows, BATCH = 8;
   const PartNote note = a.part_note[blockIdx.x];
   if (note.parts == 0) return;
   const int gl = threadIdx.x % LANES, g = threadIdx.x / LANES, d = gl * 4;
   const int h = blockIdx.z, group = a.heads_q / a.heads_kv;
   const int local = FEW ? blockIdx.y : blockIdx.y * GROUPS + g;
-  const int row = FEW ? local : (note.place >> 1) * SLOT + local;
+  const int row = FEW ? local : (KIND == kFoldRuns ? note.place >> 1 : note.place) * SLOT + local;
   if (row >= note.rows) return;                              // FEW: the whole workgroup
   auto slot = [&](int s) -> int64_t {
-    const int64_t at = (int64_t)((FEW ? note.place : (int)blockIdx.x) + s) * a.heads_kv + h;
-    return (FEW ? at : at * 2 + (s ? 0 : note.place & 1)) * SLOT + local;
+    const int64_t at = FEW                 ? note.place + s
+                       : KIND == kFoldTree ? (int64_t)blockIdx.x + (int64_t)s * note.step
+                                           : ((int64_t)blockIdx.x + s) * 2 + (s ? 0 : note.place & 1);
+    return (at * a.heads_kv + h) * SLOT + local;
   };
   float top = -INFINITY;
   for (int s = gl; s < note.parts; s += LANES) top = fmaxf(top, a.part_ml[slot(s) * 2]);
@@ -697,7 +900,13 @@ int few_target(const AttnArgs& a) {
   const int resident = device_cus() * (a.head_dim == 256 ? 1 : 2);
   return resident / a.heads_kv > 1 ? resident / a.heads_kv : 1;
 }
-int64_t few_slots(const AttnArgs& a) { return (int64_t)few_target(a) + a.entries; }
+// Rounds of slots: more than one only where entries are many against the target.
+int rounds_of(const AttnArgs& a, int target) { return 2 * (int64_t)a.entries > target ? kRounds : 1; }
+
+int64_t few_slots(const AttnArgs& a) {
+  const int64_t slots = (int64_t)rounds_of(a, few_target(a)) * few_target(a);
+  return slots > a.entries ? slots : a.entries;
+}
 
 // Runs per key head of the many-row kernel: its resident workgroups over the heads.
 int many_target(const AttnArgs& a) {
@@ -712,8 +921,16 @@ struct Parts {
 };
 
 Parts part_bytes(const AttnArgs& a) {
-  const int64_t slots = few_rows(a) ? few_slots(a) : many_target(a);
-  const int64_t rows = slots * a.heads_kv * (few_rows(a) ? kFewRows : 2 * (a.head_dim == 256 ? Many<256>::kRows : Many<128>::kRows));
+  int64_t slots, rows;                                       // notes; rows of partial outputs a head
+  if (few_rows(a)) {
+    slots = few_slots(a);
+    rows = slots * kFewRows;
+  } else {
+    const int64_t of_slot = a.head_dim == 256 ? Many<256>::kRows : Many<128>::kRows;
+    slots = (int64_t)many_target(a) * (a.tree ? rounds_of(a, many_target(a)) : 1);
+    rows = slots * (a.tree ? 1 : 2) * of_slot;
+  }
+  rows *= a.heads_kv;
   return {round256((size_t)rows * a.head_dim * 4), round256((size_t)rows * 8), round256((size_t)slots * sizeof(PartNote))};
 }
 
@@ -721,9 +938,10 @@ template <typename T, int D, bool TREE>
 hipError_t launch_typed(AttnArgs& a, hipStream_t stream) {
   if (few_rows(a)) {
     a.target = few_target(a);
+    a.rounds = rounds_of(a, a.target);
     const unsigned slots = (unsigned)few_slots(a), rows = (unsigned)(a.max_q * (a.heads_q / a.heads_kv));
     attention_few_kernel<T, D, TREE><<<dim3(slots, a.heads_kv), kThreads, 0, stream>>>(a);
-    attention_fold_kernel<T, D, true><<<dim3(a.entries, rows, a.heads_kv), kThreads, 0, stream>>>(a);
+    attention_fold_kernel<T, D, kFoldFew><<<dim3(a.entries, rows, a.heads_kv), kThreads, 0, stream>>>(a);
     return hipGetLastError();
   }
   constexpr size_t lds = 2 * 2 * (size_t)kManyKeys * D * 2;
@@ -731,15 +949,17 @@ hipError_t launch_typed(AttnArgs& a, hipStream_t stream) {
                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (ready != hipSuccess) return ready;
   a.target = many_target(a);
+  a.rounds = rounds_of(a, a.target);
   attention_many_kernel<T, D, TREE><<<(unsigned)(a.target * a.heads_kv), Many<D>::kThreads, lds, stream>>>(a);
-  attention_fold_kernel<T, D, false>
-      <<<dim3((unsigned)a.target, Many<D>::kRows * D / (4 * kThreads), a.heads_kv), kThreads, 0, stream>>>(a);
+  const unsigned notes = (unsigned)(TREE ? a.target * a.rounds : a.target);
+  attention_fold_kernel<T, D, TREE ? kFoldTree : kFoldRuns>
+      <<<dim3(notes, Many<D>::kRows * D / (4 * kThreads), a.heads_kv), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
 template <typename T, int D>
 hipError_t launch_masked(AttnArgs& a, hipStream_t stream) {
-  return a.ancestors ? launch_typed<T, D, true>(a, stream) : launch_typed<T, D, false>(a, stream);
+  return a.tree ? launch_typed<T, D, true>(a, stream) : launch_typed<T, D, false>(a, stream);
 }
 
 template <typename T>

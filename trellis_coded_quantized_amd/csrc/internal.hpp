@@ -87,10 +87,11 @@ int api_hip(const char* fn, hipError_t e);
 struct PartNote {
   int parts;                  // 0: nothing to fold here
   int first, rows;            // the entry's first row of q, its rows per key head
-  int place;                  // few rows: slot of the first part; many: row tile << 1 | place of the first part
+  int place;                  // few rows: slot of the first part; trees: row tile; else row tile << 1 | place
+  int step;                   // trees: slots from part to part
 };
 
-// One attention call.  TREE: `ancestors` is set, window and sinks are 0.
+// One attention call.  tree: `ancestors` is set, window and sinks are 0.
 struct AttnArgs {
   const uint16_t* q;
   const uint16_t* k;
@@ -108,7 +109,9 @@ struct AttnArgs {
   uint32_t pages;
   int entries, max_q, heads_q, heads_kv, head_dim, page_log2;
   int window, sinks, fp16;
+  int tree;
   int target;                 // workgroups per key head that the keys are cut for
+  int rounds;                 // slots a workgroup where units are many
   float scale;
 };
 
