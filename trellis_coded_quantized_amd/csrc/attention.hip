@@ -342,21 +342,17 @@ struct Many {
 };
 
 // Scheduling hint for the code around it: a few operand reads ahead, then every
-// matrix instruction followed by the next read and the block's other work.
-template <int MFMAS, int VALU, int TRANS, int FETCHES, int STORES, int I = 0>
+// matrix instruction followed by the next read and vector instructions.
+template <int MFMAS, int VALU, int TRANS>
 __device__ __forceinline__ void interleave() {
   constexpr int AHEAD = 4;
-  if constexpr (I == 0) __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
-  if constexpr (I < MFMAS) {
+  __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+#pragma unroll
+  for (int i = 0; i < MFMAS; ++i) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    if constexpr (I < MFMAS - AHEAD) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-    if constexpr (VALU > 0) __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
-    if constexpr (TRANS > 0) __builtin_amdgcn_sched_group_barrier(0x400, TRANS, 0);
-    constexpr int LOADS = (I + 1) * FETCHES / MFMAS - I * FETCHES / MFMAS;
-    constexpr int WRITES = (I + 1) * STORES / MFMAS - I * STORES / MFMAS;
-    if constexpr (LOADS > 0) __builtin_amdgcn_sched_group_barrier(0x020, LOADS, 0);
-    if constexpr (WRITES > 0) __builtin_amdgcn_sched_group_barrier(0x200, WRITES, 0);
-    interleave<MFMAS, VALU, TRANS, FETCHES, STORES, I + 1>();
+    if (i < MFMAS - AHEAD) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    if (VALU) __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+    if (TRANS) __builtin_amdgcn_sched_group_barrier(0x400, TRANS, 0);
   }
 }
 
@@ -645,7 +641,11 @@ __global__ __launch_bounds__(Many<D>::kThreads) void attention_many_kernel(AttnA
     for (int t = 0; t < DT; ++t) o[t] = f32x16{};
     Running st{-INFINITY, 0.0f};
 
-    u32x4v in_k[PER], in_v[PER];                             // a thread's granules of the next tile on their way
+    // A thread's granules of the next tile on their way.  Both operands are
+    // under way for a whole tile where the registers allow it; at D = 256 they
+    // take turns in one set, half a tile each.
+    constexpr bool TURNS = D == 256;
+    u32x4v in[PER], in_v[TURNS ? 1 : PER];
     // The page of each of a tile's keys, one key a lane.
     auto pages_of = [&](int t) {
       const int key = list.key<KT>(min(t, t1 - 1)) + lane;
@@ -654,15 +654,17 @@ __global__ __launch_bounds__(Many<D>::kThreads) void attention_many_kernel(AttnA
     const uint32_t page_elems = (uint32_t)(a.heads_kv * D) << a.page_log2, head_at = (uint32_t)(h * D) << a.page_log2;
     // keys: granule g of the tile is dimension block g / 64 of key g % 64, so
     // a thread keeps its key
+    auto fetch_keys = [&](int t, int32_t pk, u32x4v (&in)[PER]) {
+      const uint16_t* kp = a.k + (uint64_t)page_in_pool(pk, a.pages) * page_elems + head_at +
+                           (((list.key<KT>(t) + lane) & pmask) + wave * P) * 8;
+#pragma unroll
+      for (int n = 0; n < PER; ++n) in[n] = *reinterpret_cast<const u32x4v*>(kp + n * WAVES * P * 8);
+    };
     // values: granule g is token block g / D of dimension g % D, one token
     // block a wave, whose address the lane of the block's first key works out
-    auto fetch = [&](int t, int32_t pk) {
-      const uint64_t at_page = (uint64_t)page_in_pool(pk, a.pages) * page_elems + head_at;
-      const int off = (list.key<KT>(t) + lane) & pmask;
-      const uint16_t* kp = a.k + at_page + (off + wave * P) * 8;
-#pragma unroll
-      for (int n = 0; n < PER; ++n) in_k[n] = *reinterpret_cast<const u32x4v*>(kp + n * WAVES * P * 8);
-      const uint64_t block = (uint64_t)(a.v + at_page + (off >> 3) * D * 8);
+    auto fetch_values = [&](int t, int32_t pk, u32x4v (&in)[PER]) {
+      const uint64_t block = (uint64_t)(a.v + (uint64_t)page_in_pool(pk, a.pages) * page_elems + head_at +
+                                        (((list.key<KT>(t) + lane) & pmask) >> 3) * D * 8);
 #pragma unroll
       for (int n = 0; n < PER; ++n) {
         const int g = n * THREADS + wave * 64, from = g / D * 8;
@@ -670,29 +672,20 @@ __global__ __launch_bounds__(Many<D>::kThreads) void attention_many_kernel(AttnA
         const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(block >> 32), from);
         const auto rsrc =
             __builtin_amdgcn_make_buffer_rsrc((void*)(((uint64_t)hi << 32) | lo), 0, D * 16, kRawBufferWord3);
-        in_v[n] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, lane * 16, g % D * 16, 0);
+        in[n] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, lane * 16, g % D * 16, 0);
       }
     };
-    auto store = [&](int buf) {
+    auto store_keys = [&](int buf, const u32x4v (&in)[PER]) {
 #pragma unroll
-      for (int n = 0; n < PER; ++n) {
-        lds[buf * 2 * GRAN + n * THREADS + tid] = in_k[n];
-        lds[(buf * 2 + 1) * GRAN + n * THREADS + tid] = in_v[n];
-      }
+      for (int n = 0; n < PER; ++n) lds[buf * 2 * GRAN + n * THREADS + tid] = in[n];
     };
-    // A tile that some row does not see in full has its values cleaned in
-    // place before it is used; s_bad is the last tile where that changed any.
-    auto clean = [&](int buf, int t) {
-      if (seen_by_all.tile(list.key<KT>(t), KT)) return;
-      u32x4v v[PER];
-#pragma unroll
-      for (int n = 0; n < PER; ++n) v[n] = lds[(buf * 2 + 1) * GRAN + n * THREADS + tid];
-      if (drop_nonfinite<T>(v)) {
-        s_bad[buf] = t;
-#pragma unroll
-        for (int n = 0; n < PER; ++n) lds[(buf * 2 + 1) * GRAN + n * THREADS + tid] = v[n];
+    // s_bad: the last tile whose values had to be cleaned
+    auto store_values = [&](int buf, int t, u32x4v (&in)[PER]) {
+      if (!seen_by_all.tile(list.key<KT>(t), KT)) {
+        if (drop_nonfinite<T>(in)) s_bad[buf] = t;
       }
-      lds_barrier();
+#pragma unroll
+      for (int n = 0; n < PER; ++n) lds[(buf * 2 + 1) * GRAN + n * THREADS + tid] = in[n];
     };
     auto rescale = [&](float alpha) {
       settle(o);
@@ -707,30 +700,38 @@ __global__ __launch_bounds__(Many<D>::kThreads) void attention_many_kernel(AttnA
     lds_barrier();
     int32_t page = 0;
     if (t0 < t1) {
-      fetch(t0, pages_of(t0));
+      u32x4v too[PER];
+      page = pages_of(t0);
+      fetch_keys(t0, page, in);
+      fetch_values(t0, page, too);
       page = pages_of(t0 + 1);
-      store(0);
-      lds_barrier();
-      clean(0, t0);
+      store_keys(0, in);
+      store_values(0, t0, too);
     }
+    lds_barrier();
     const int krow = tile_key_of_row(col);
     waitcnt_vm<0>();         // q has arrived: waits inside the loop are for the tiles' loads only
     for (int t = t0; t < t1; ++t) {
-      const int buf = (t - t0) & 1, kb = list.key<KT>(t), next = min(t + 1, t1 - 1);
+      const int buf = (t - t0) & 1, kb = list.key<KT>(t);
+      const bool more = t + 1 < t1;
       const u32x4v* kt = lds + buf * 2 * GRAN + half * KT + krow;        // [2 s + half][32 x + key]
       const u32x4v* vt = lds + (buf * 2 + 1) * GRAN + half * D + col;    // [4 x + 2 s + half][dimension]
+      if (more) {
+        fetch_keys(t + 1, page, in);
+        if constexpr (!TURNS) {
+          fetch_values(t + 1, page, in_v);
+          page = pages_of(t + 2);
+        }
+      }
       const bool open = seen_by_wave.tile(kb, KT);
-      // The next tile's loads and stores stand among the matrix instructions,
-      // without a branch (after the last tile it is fetched again).
-      if (w0 < rows && reach.touches(kb, KT)) {
-        uint64_t seen = 0;
-        f32x16 s0 = f32x16{}, s1 = f32x16{};
-        u32x4v p0[2], p1[2];
-        fetch(next, page);
-        page = pages_of(t + 2);
+      const bool wave_live = w0 < rows && reach.touches(kb, KT);
+      uint64_t seen = 0;
+      f32x16 s0 = f32x16{}, s1 = f32x16{};
+      u32x4v p0[2], p1[2];
+      if (wave_live) {
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) s0 = T::mfma(kt[2 * s * KT], q[s], s0);
-        interleave<STEPS, 4, 0, 2 * PER + 1, 0>();
+        interleave<STEPS, 0, 0>();
         if (!open) {
           seen = mask.template bits<TREE>(kb);
           cut_scores(s0, (uint32_t)seen);
@@ -740,20 +741,28 @@ __global__ __launch_bounds__(Many<D>::kThreads) void attention_many_kernel(AttnA
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) s1 = T::mfma(kt[2 * s * KT + 32], q[s], s1);
         float sum = weigh<T>(s0, c, st, p0);
-        interleave<STEPS, 56 / STEPS, 16 / STEPS, 0, 0>();
+        interleave<STEPS, 56 / STEPS, 16 / STEPS>();
         keep_here(p0, sum);
         st.l += sum;
+      }
+      if constexpr (TURNS) {
+        if (more) {
+          store_keys(buf ^ 1, in);
+          fetch_values(t + 1, page, in);
+          page = pages_of(t + 2);
+        }
+      }
+      if (wave_live) {
         if (!open) cut_scores(s1, (uint32_t)(seen >> 32));
-        top = row_top(s1, c);
-        float alpha = 1.0f;
+        float top = row_top(s1, c), alpha = 1.0f;
         const bool moved = must_move(top, st);
         if (moved) alpha = move_bound(top, st);
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
           for (int d = 0; d < DT; ++d) o[d] = T::mfma(vt[2 * s * D + d * 32], p0[s], o[d]);
-        sum = weigh<T>(s1, c, st, p1);
-        interleave<2 * DT, 56 / (2 * DT), 16 / (2 * DT), 0, 0>();
+        float sum = weigh<T>(s1, c, st, p1);
+        interleave<2 * DT, 56 / (2 * DT), 16 / (2 * DT)>();
         keep_here(p1, sum);
         if (moved) rescale(alpha);                           // the first block was weighed with the earlier bound
         st.l += sum;
@@ -761,20 +770,22 @@ __global__ __launch_bounds__(Many<D>::kThreads) void attention_many_kernel(AttnA
         for (int s = 0; s < 2; ++s)
 #pragma unroll
           for (int d = 0; d < DT; ++d) o[d] = T::mfma(vt[(4 + 2 * s) * D + d * 32], p1[s], o[d]);
-        store(buf ^ 1);
-        interleave<2 * DT, 0, 0, 0, 2 * PER>();
+        interleave<2 * DT, 0, 0>();
         settle(o);
         if (s_bad[buf] == t) {
           add_nonfinite<T, D, TREE>(a.v + head_at, e.pages, a.pages, page_elems, a.page_log2, mask, kb, KT, o);
           settle(o);
         }
-      } else {
-        fetch(next, page);
-        page = pages_of(t + 2);
-        store(buf ^ 1);
+      }
+      if (more) {
+        if constexpr (TURNS) {
+          store_values(buf ^ 1, t + 1, in);
+        } else {
+          store_keys(buf ^ 1, in);
+          store_values(buf ^ 1, t + 1, in_v);
+        }
       }
       lds_barrier();
-      if (t + 1 < t1) clean(buf ^ 1, t + 1);
     }
 
     settle(o);
