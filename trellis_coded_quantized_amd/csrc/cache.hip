@@ -16,13 +16,15 @@ namespace {
 constexpr int kPlan = 1024;               // threads of the one workgroup that hands out pages
 constexpr int kPlanWaves = kPlan / 64;
 
-// Whether entry b of a list names a sequence of the state that no earlier entry names.
+// Whether entry b of a list names a sequence of the state that no earlier
+// entry names.  Called by a whole wave, whose lanes compare 64 entries at a
+// time: one lane by itself waits a memory latency for each (8 us of a
+// reservation for 16 of 48 sequences).
 __device__ __forceinline__ bool first_of_its_name(const int32_t* ids, int b, int64_t seqs) {
   const int32_t id = ids[b];
-  if (id < 0 || id >= seqs) return false;
-  for (int j = 0; j < b; ++j)
-    if (ids[j] == id) return false;
-  return true;
+  bool known = false;
+  for (int j = threadIdx.x & 63; j < b; j += 64) known |= ids[j] == id;
+  return id >= 0 && id < seqs && __ballot(known) == 0;
 }
 
 // Exclusive sum over the workgroup's threads; `total` for all.
@@ -73,9 +75,27 @@ __device__ __forceinline__ int find_free(const int32_t* refs, uint32_t pages, in
 
 // ---- reserve -------------------------------------------------------------
 
+// The slot of token t: the last entry that starts at or before it owns it.
+__device__ __forceinline__ int32_t slot_of(const CacheArgs& c, const int32_t* seq_ids, int n, const int32_t* q_start,
+                                           const int32_t* granted, int64_t t) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (q_start[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  if (!granted[lo] || t < q_start[lo] || t >= q_start[lo + 1]) return -1;
+  const int64_t at = max(c.lengths[seq_ids[lo]], 0) + t - max(q_start[lo], 0);
+  const int32_t page = c.table[(int64_t)seq_ids[lo] * c.width + (at >> c.page_log2)];
+  return page_ok(page, c.pages) ? (int32_t)(((int64_t)page << c.page_log2) + (at & ((1 << c.page_log2) - 1))) : -1;
+}
+
+// One workgroup hands out the pages.  With SLOTS it writes the tokens' slots
+// too, which saves a launch for a step that decodes.
+template <bool SLOTS>
 __global__ __launch_bounds__(kPlan) void reserve_plan_kernel(CacheArgs c, const int32_t* seq_ids, int n,
                                                              const int32_t* q_start, int64_t tokens, int32_t* granted,
-                                                             int32_t* list) {
+                                                             int32_t* list, int32_t* slots) {
   __shared__ int s_need[kCacheMaxEntries], s_at[kCacheMaxEntries], s_sums[kPlanWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t room = c.width << c.page_log2;
@@ -123,6 +143,10 @@ __global__ __launch_bounds__(kPlan) void reserve_plan_kernel(CacheArgs c, const 
       next += __popcll(votes);
     }
   }
+  if (SLOTS) {
+    __syncthreads();
+    for (int64_t t = tid; t < tokens; t += kPlan) slots[t] = slot_of(c, seq_ids, n, q_start, granted, t);
+  }
 }
 
 __global__ __launch_bounds__(256) void reserve_slots_kernel(CacheArgs c, const int32_t* seq_ids, int n,
@@ -130,19 +154,7 @@ __global__ __launch_bounds__(256) void reserve_slots_kernel(CacheArgs c, const i
                                                             const int32_t* granted, int32_t* slots) {
   const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (t >= tokens) return;
-  int lo = 0, hi = n;                      // the last entry that starts at or before t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (q_start[mid] <= t) lo = mid;
-    else hi = mid;
-  }
-  int32_t slot = -1;
-  if (granted[lo] && t >= q_start[lo] && t < q_start[lo + 1]) {
-    const int64_t at = max(c.lengths[seq_ids[lo]], 0) + t - max(q_start[lo], 0);
-    const int32_t page = c.table[(int64_t)seq_ids[lo] * c.width + (at >> c.page_log2)];
-    if (page_ok(page, c.pages)) slot = (int32_t)(((int64_t)page << c.page_log2) + (at & ((1 << c.page_log2) - 1)));
-  }
-  slots[t] = slot;
+  slots[t] = slot_of(c, seq_ids, n, q_start, granted, t);
 }
 
 // ---- fork ----------------------------------------------------------------
@@ -265,8 +277,28 @@ __global__ __launch_bounds__(256) void fork_write_kernel(CacheArgs c, const int3
 // ---- accept --------------------------------------------------------------
 // Row length + j becomes what row length + path[j] was: one workgroup per
 // (sequence, layer, head) reads all its rows into LDS before it writes any.
-__global__ __launch_bounds__(256) void accept_kernel(CacheArgs c, const int32_t* seq_ids, const int32_t* path,
-                                                     int max_path, const int32_t* counts) {
+// Where the new lengths go to an array of their own, the workgroups past the
+// list's end write them; in place that has to wait for all readers.
+__device__ __forceinline__ void accept_lengths(const CacheArgs& c, const int32_t* seq_ids, int n, int max_path,
+                                               const int32_t* counts, int32_t* new_lengths) {
+  const int waves = blockDim.x >> 6;
+  if (new_lengths != c.lengths) {
+    for (int64_t s = threadIdx.x; s < c.seqs; s += blockDim.x) new_lengths[s] = c.lengths[s];
+    __syncthreads();
+  }
+  for (int b = threadIdx.x >> 6; b < n; b += waves) {
+    if (!first_of_its_name(seq_ids, b, c.seqs) || (threadIdx.x & 63)) continue;
+    const int64_t len = max(c.lengths[seq_ids[b]], 0);
+    new_lengths[seq_ids[b]] = (int32_t)min(len + min(max(counts[b], 0), max_path), c.width << c.page_log2);
+  }
+}
+
+__global__ __launch_bounds__(256) void accept_kernel(CacheArgs c, const int32_t* seq_ids, int n, const int32_t* path,
+                                                     int max_path, const int32_t* counts, int32_t* new_lengths) {
+  if ((int)blockIdx.x == n) {
+    if (blockIdx.y == 0 && blockIdx.z == 0) accept_lengths(c, seq_ids, n, max_path, counts, new_lengths);
+    return;
+  }
   extern __shared__ __align__(16) u32x4v lds[];              // keys [row][D / 8], values [row][D / 8]
   const int b = blockIdx.x, layer = blockIdx.y, h = blockIdx.z, tid = threadIdx.x;
   const int count = min(max(counts[b], 0), max_path);
@@ -308,14 +340,7 @@ __global__ __launch_bounds__(256) void accept_kernel(CacheArgs c, const int32_t*
 __global__ __launch_bounds__(kPlan) void accept_lengths_kernel(CacheArgs c, const int32_t* seq_ids, int n,
                                                                int max_path, const int32_t* counts,
                                                                int32_t* new_lengths) {
-  const int64_t room = c.width << c.page_log2;
-  if (new_lengths != c.lengths)
-    for (int64_t s = threadIdx.x; s < c.seqs; s += kPlan) new_lengths[s] = c.lengths[s];
-  __syncthreads();
-  const int b = threadIdx.x;
-  if (b >= n || !first_of_its_name(seq_ids, b, c.seqs)) return;
-  const int64_t len = max(c.lengths[seq_ids[b]], 0);
-  new_lengths[seq_ids[b]] = (int32_t)min(len + min(max(counts[b], 0), max_path), room);
+  accept_lengths(c, seq_ids, n, max_path, counts, new_lengths);
 }
 
 // ---- free ----------------------------------------------------------------
@@ -344,11 +369,14 @@ size_t cache_reserve_workspace_bytes(const CacheArgs& c, int n) {
 hipError_t launch_cache_reserve(const CacheArgs& c, const int32_t* seq_ids, int n, const int32_t* q_start,
                                 int64_t tokens, int32_t* slots, int32_t* granted, void* workspace,
                                 hipStream_t stream) {
-  reserve_plan_kernel<<<1, kPlan, 0, stream>>>(c, seq_ids, n, q_start, tokens, granted,
-                                               reinterpret_cast<int32_t*>(workspace));
-  if (tokens > 0)
+  int32_t* list = reinterpret_cast<int32_t*>(workspace);
+  if (tokens <= kPlan) {
+    reserve_plan_kernel<true><<<1, kPlan, 0, stream>>>(c, seq_ids, n, q_start, tokens, granted, list, slots);
+  } else {
+    reserve_plan_kernel<false><<<1, kPlan, 0, stream>>>(c, seq_ids, n, q_start, tokens, granted, list, slots);
     reserve_slots_kernel<<<(unsigned)((tokens + 255) / 256), 256, 0, stream>>>(c, seq_ids, n, q_start, tokens, granted,
                                                                                slots);
+  }
   return hipGetLastError();
 }
 
@@ -371,8 +399,11 @@ hipError_t launch_cache_fork(const CacheArgs& c, const int32_t* parents, const i
 hipError_t launch_cache_accept(const CacheArgs& c, const int32_t* seq_ids, int n, const int32_t* path, int max_path,
                                const int32_t* counts, int32_t* new_lengths, hipStream_t stream) {
   const size_t lds = (size_t)max_path * c.head_dim * 4;
-  accept_kernel<<<dim3(n, c.layers, c.heads), 256, lds, stream>>>(c, seq_ids, path, max_path, counts);
-  accept_lengths_kernel<<<1, kPlan, 0, stream>>>(c, seq_ids, n, max_path, counts, new_lengths);
+  const bool in_place = new_lengths == c.lengths;
+  accept_kernel<<<dim3(n + !in_place, c.layers, c.heads), 256, lds, stream>>>(c, seq_ids, n, path, max_path, counts,
+                                                                              new_lengths);
+  if (in_place)
+    accept_lengths_kernel<<<1, kPlan, 0, stream>>>(c, seq_ids, n, max_path, counts, new_lengths);
   return hipGetLastError();
 }
 
