@@ -828,24 +828,28 @@ __global__ __launch_bounds__(Many<D>::kThreads) void attention_many_kernel(AttnA
 //   many rows, trees: notes by the slot of the first part, parts every `step` slots.
 //   many rows, consecutive tokens: notes by the run that begins the unit; the
 //     first part is in place 0 or 1 of that run, the others in place 0 of the
-//     runs after it.  1024 / D rows a workgroup for both.
+//     runs after it.  1024 / D rows a workgroup for both.  Notes are the slowest
+//     dimension of the grid: most of a short call's are empty, and as the
+//     fastest they left its work to one XCD (one tree of 64 tokens, 4096 keys,
+//     32 / 8 heads of 128: 34 us).
 enum FoldKind { kFoldFew, kFoldTree, kFoldRuns };
 
 template <typename T, int D, FoldKind KIND>
 __global__ __launch_bounds__(kThreads) void attention_fold_kernel(AttnArgs a) {
   constexpr bool FEW = KIND == kFoldFew;
   constexpr int LANES = D / 4, GROUPS = kThreads / LANES, SLOT = FEW ? kFewRows : Many<D>::kRows, BATCH = 8;
-  const PartNote note = a.part_note[blockIdx.x];
+  const int at_note = FEW ? blockIdx.x : blockIdx.z;
+  const PartNote note = a.part_note[at_note];
   if (note.parts == 0) return;
   const int gl = threadIdx.x % LANES, g = threadIdx.x / LANES, d = gl * 4;
-  const int h = blockIdx.z, group = a.heads_q / a.heads_kv;
-  const int local = FEW ? blockIdx.y : blockIdx.y * GROUPS + g;
+  const int h = FEW ? blockIdx.z : blockIdx.y, group = a.heads_q / a.heads_kv;
+  const int local = FEW ? blockIdx.y : blockIdx.x * GROUPS + g;
   const int row = FEW ? local : (KIND == kFoldRuns ? note.place >> 1 : note.place) * SLOT + local;
   if (row >= note.rows) return;                              // FEW: the whole workgroup
   auto slot = [&](int s) -> int64_t {
     const int64_t at = FEW                 ? note.place + s
-                       : KIND == kFoldTree ? (int64_t)blockIdx.x + (int64_t)s * note.step
-                                           : ((int64_t)blockIdx.x + s) * 2 + (s ? 0 : note.place & 1);
+                       : KIND == kFoldTree ? (int64_t)at_note + (int64_t)s * note.step
+                                           : ((int64_t)at_note + s) * 2 + (s ? 0 : note.place & 1);
     return (at * a.heads_kv + h) * SLOT + local;
   };
   float top = -INFINITY;
@@ -953,7 +957,7 @@ hipError_t launch_typed(AttnArgs& a, hipStream_t stream) {
   attention_many_kernel<T, D, TREE><<<(unsigned)(a.target * a.heads_kv), Many<D>::kThreads, lds, stream>>>(a);
   const unsigned notes = (unsigned)(TREE ? a.target * a.rounds : a.target);
   attention_fold_kernel<T, D, TREE ? kFoldTree : kFoldRuns>
-      <<<dim3(notes, Many<D>::kRows * D / (4 * kThreads), a.heads_kv), kThreads, 0, stream>>>(a);
+      <<<dim3(Many<D>::kRows * D / (4 * kThreads), a.heads_kv, notes), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
