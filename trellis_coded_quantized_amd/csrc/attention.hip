@@ -3,6 +3,7 @@
 // (prompt chunks, wide trees), and the fold of split keys.
 #include "attention.hpp"
 #include "copy_ring.hpp"
+#include <type_traits>
 
 namespace trellis {
 namespace {
@@ -329,32 +330,21 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_few_kern
 // contiguous across lanes and nothing is transposed.  At D = 256 a wave's
 // outputs and queries fill a SIMD's registers alone, and it is 128 rows.
 //
-// A tile is two blocks of 32 keys.  The second block's scores are computed
-// under the first block's exponentials, and the first block's product with the
-// values under the second's.  (Taking weights under the old bound while the
-// maximum is still being worked out, and again where it moved, measured
-// slower at D = 128: 830 against 908 TFLOP/s.  So did two workgroups of 128
-// rows a compute unit: 821.)
+// A tile is two blocks of 32 keys.  The product with the values runs one tile
+// behind the scores: a block's maximum is taken under the next block's scores,
+// its weights under the product of the block before it, so all vector work
+// has matrix work beside it, from the same wave at D = 256 where there is no
+// other.  Loads of a tile are under way for a whole period.  The order is
+// written out and pinned, an operand read four to six matrix instructions
+// before its use; hints to the scheduler left most reads waited for at once
+// (2048 tokens, 18432 keys, 24 / 4 heads of 256: 644 TFLOP/s against 889;
+// 32 / 8 heads of 128: 906 against 985).  Two workgroups of 128 rows a compute
+// unit were slower than one of 256.
 template <int D>
 struct Many {
   static constexpr int kWaves = D == 256 ? 4 : 8;
   static constexpr int kThreads = 64 * kWaves, kRows = 32 * kWaves;
 };
-
-// Scheduling hint for the code around it: a few operand reads ahead, then every
-// matrix instruction followed by the next read and vector instructions.
-template <int MFMAS, int VALU, int TRANS>
-__device__ __forceinline__ void interleave() {
-  constexpr int AHEAD = 4;
-  __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
-#pragma unroll
-  for (int i = 0; i < MFMAS; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    if (i < MFMAS - AHEAD) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-    if (VALU) __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
-    if (TRANS) __builtin_amdgcn_sched_group_barrier(0x400, TRANS, 0);
-  }
-}
 
 // Weights that were taken before this point, not where they are used.
 __device__ __forceinline__ void keep_here(u32x4v (&p)[2], float& sum) {
@@ -620,13 +610,11 @@ __global__ __launch_bounds__(Many<D>::kThreads) void attention_many_kernel(AttnA
 
     const int row = r0 + wave * 32 + col;
     RowMask mask;
-    // What all rows of the workgroup see (their values need no cleaning), what
-    // all rows of the wave see, and what any row of the wave sees: a wave
-    // only carries tiles outside that.
+    // What all rows of the workgroup see (their values need no cleaning), and
+    // what all rows of the wave see.
     const OpenKeys seen_by_all = open_keys<TREE>(a, e, i0, i1);
     const int w0 = r0 + wave * 32, j0 = min(w0, rows - 1) / group, j1 = min(w0 + 31, rows - 1) / group;
     const OpenKeys seen_by_wave = open_keys<TREE>(a, e, j0, j1);
-    const OpenKeys reach = reach_keys<TREE>(a, e, j0, j1);
     u32x4v q[STEPS];
     {
       const bool live = row < rows;
@@ -641,11 +629,9 @@ __global__ __launch_bounds__(Many<D>::kThreads) void attention_many_kernel(AttnA
     for (int t = 0; t < DT; ++t) o[t] = f32x16{};
     Running st{-INFINITY, 0.0f};
 
-    // A thread's granules of the next tile on their way.  Both operands are
-    // under way for a whole tile where the registers allow it; at D = 256 they
-    // take turns in one set, half a tile each.
-    constexpr bool TURNS = D == 256;
-    u32x4v in[PER], in_v[TURNS ? 1 : PER];
+    // A thread's granules on their way to LDS: of the keys one tile, of the
+    // values the tile before it.
+    u32x4v in_k[PER], in_v[PER];
     // The page of each of a tile's keys, one key a lane.
     auto pages_of = [&](int t) {
       const int key = list.key<KT>(min(t, t1 - 1)) + lane;
@@ -654,38 +640,26 @@ __global__ __launch_bounds__(Many<D>::kThreads) void attention_many_kernel(AttnA
     const uint32_t page_elems = (uint32_t)(a.heads_kv * D) << a.page_log2, head_at = (uint32_t)(h * D) << a.page_log2;
     // keys: granule g of the tile is dimension block g / 64 of key g % 64, so
     // a thread keeps its key
-    auto fetch_keys = [&](int t, int32_t pk, u32x4v (&in)[PER]) {
-      const uint16_t* kp = a.k + (uint64_t)page_in_pool(pk, a.pages) * page_elems + head_at +
-                           (((list.key<KT>(t) + lane) & pmask) + wave * P) * 8;
-#pragma unroll
-      for (int n = 0; n < PER; ++n) in[n] = *reinterpret_cast<const u32x4v*>(kp + n * WAVES * P * 8);
+    auto keys_at = [&](int t, int32_t page) {
+      return a.k + (uint64_t)page_in_pool(page, a.pages) * page_elems + head_at +
+             (((list.key<KT>(min(t, t1 - 1)) + lane) & pmask) + wave * P) * 8;
+    };
+    auto load_keys = [&](const uint16_t* at, int n) {
+      in_k[n] = *reinterpret_cast<const u32x4v*>(at + n * WAVES * P * 8);
     };
     // values: granule g is token block g / D of dimension g % D, one token
     // block a wave, whose address the lane of the block's first key works out
-    auto fetch_values = [&](int t, int32_t pk, u32x4v (&in)[PER]) {
-      const uint64_t block = (uint64_t)(a.v + (uint64_t)page_in_pool(pk, a.pages) * page_elems + head_at +
-                                        (((list.key<KT>(t) + lane) & pmask) >> 3) * D * 8);
-#pragma unroll
-      for (int n = 0; n < PER; ++n) {
-        const int g = n * THREADS + wave * 64, from = g / D * 8;
-        const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)block, from);
-        const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(block >> 32), from);
-        const auto rsrc =
-            __builtin_amdgcn_make_buffer_rsrc((void*)(((uint64_t)hi << 32) | lo), 0, D * 16, kRawBufferWord3);
-        in[n] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, lane * 16, g % D * 16, 0);
-      }
+    auto values_at = [&](int t, int32_t page) {
+      return (uint64_t)(a.v + (uint64_t)page_in_pool(page, a.pages) * page_elems + head_at +
+                        (((list.key<KT>(min(t, t1 - 1)) + lane) & pmask) >> 3) * D * 8);
     };
-    auto store_keys = [&](int buf, const u32x4v (&in)[PER]) {
-#pragma unroll
-      for (int n = 0; n < PER; ++n) lds[buf * 2 * GRAN + n * THREADS + tid] = in[n];
-    };
-    // s_bad: the last tile whose values had to be cleaned
-    auto store_values = [&](int buf, int t, u32x4v (&in)[PER]) {
-      if (!seen_by_all.tile(list.key<KT>(t), KT)) {
-        if (drop_nonfinite<T>(in)) s_bad[buf] = t;
-      }
-#pragma unroll
-      for (int n = 0; n < PER; ++n) lds[(buf * 2 + 1) * GRAN + n * THREADS + tid] = in[n];
+    auto load_values = [&](uint64_t at, int n) {
+      const int g = n * THREADS + wave * 64, from = g / D * 8;
+      const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)at, from);
+      const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(at >> 32), from);
+      const auto rsrc =
+          __builtin_amdgcn_make_buffer_rsrc((void*)(((uint64_t)hi << 32) | lo), 0, D * 16, kRawBufferWord3);
+      in_v[n] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, lane * 16, g % D * 16, 0);
     };
     auto rescale = [&](float alpha) {
       settle(o);
@@ -697,95 +671,197 @@ __global__ __launch_bounds__(Many<D>::kThreads) void attention_many_kernel(AttnA
     };
 
     if (tid < 2) s_bad[tid] = -1;
-    lds_barrier();
-    int32_t page = 0;
+    int32_t page_v = 0, page_k = 0;                          // pages of the tiles that are loaded next
     if (t0 < t1) {
-      u32x4v too[PER];
-      page = pages_of(t0);
-      fetch_keys(t0, page, in);
-      fetch_values(t0, page, too);
-      page = pages_of(t0 + 1);
-      store_keys(0, in);
-      store_values(0, t0, too);
+      const int32_t page = pages_of(t0), after = pages_of(t0 + 1);
+      page_v = after;
+      page_k = pages_of(t0 + 2);
+      const uint16_t* kp = keys_at(t0, page);
+#pragma unroll
+      for (int n = 0; n < PER; ++n) load_keys(kp, n);
+#pragma unroll
+      for (int n = 0; n < PER; ++n) lds[n * THREADS + tid] = in_k[n];
+      waitcnt_vm<0>();       // q has arrived too: waits inside the loop are for the tiles' loads only
+      kp = keys_at(t0 + 1, after);
+      const uint64_t vp = values_at(t0, page);
+#pragma unroll
+      for (int n = 0; n < PER; ++n) load_keys(kp, n);
+#pragma unroll
+      for (int n = 0; n < PER; ++n) load_values(vp, n);
     }
     lds_barrier();
     const int krow = tile_key_of_row(col);
-    waitcnt_vm<0>();         // q has arrived: waits inside the loop are for the tiles' loads only
-    for (int t = t0; t < t1; ++t) {
+    const bool has_rows = w0 < rows;
+    f32x16 sa, sb;                                           // scores of a tile's first and second block
+    u32x4v pa[2], pb[2];                                     // and their weights
+    bool open = true;
+    uint32_t seen_b = 0;
+    // Period t: scores of tile t, the product with the values of tile t - 1.
+    auto period = [&](int t, auto is_first, auto is_last) __attribute__((always_inline)) {
+      constexpr bool FIRST = decltype(is_first)::value, LAST = decltype(is_last)::value;
       const int buf = (t - t0) & 1, kb = list.key<KT>(t);
-      const bool more = t + 1 < t1;
-      const u32x4v* kt = lds + buf * 2 * GRAN + half * KT + krow;        // [2 s + half][32 x + key]
-      const u32x4v* vt = lds + (buf * 2 + 1) * GRAN + half * D + col;    // [4 x + 2 s + half][dimension]
-      if (more) {
-        fetch_keys(t + 1, page, in);
-        if constexpr (!TURNS) {
-          fetch_values(t + 1, page, in_v);
-          page = pages_of(t + 2);
-        }
+      const u32x4v* kt = lds + buf * 2 * GRAN + half * KT + krow;              // [2 s + half][32 x + key]
+      const u32x4v* vt = lds + ((buf ^ 1) * 2 + 1) * GRAN + half * D + col;    // [4 x + 2 s + half][dimension]
+      // A quarter of the staging: tile t + 1's keys and tile t's values go to
+      // LDS, and their registers take the loads of the tiles after them.
+      // Past the end the last tile is read again.
+      const uint16_t* kp = nullptr;
+      uint64_t vp = 0;
+      if constexpr (!LAST) {
+        kp = keys_at(t + 2, page_k);
+        vp = values_at(t + 1, page_v);
+        page_v = page_k;
+        page_k = pages_of(t + 3);
       }
-      const bool open = seen_by_wave.tile(kb, KT);
-      const bool wave_live = w0 < rows && reach.touches(kb, KT);
-      uint64_t seen = 0;
-      f32x16 s0 = f32x16{}, s1 = f32x16{};
-      u32x4v p0[2], p1[2];
-      if (wave_live) {
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) s0 = T::mfma(kt[2 * s * KT], q[s], s0);
-        interleave<STEPS, 0, 0>();
-        if (!open) {
-          seen = mask.template bits<TREE>(kb);
-          cut_scores(s0, (uint32_t)seen);
-        }
-        float top = row_top(s0, c);
-        if (must_move(top, st)) rescale(move_bound(top, st));
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) s1 = T::mfma(kt[2 * s * KT + 32], q[s], s1);
-        float sum = weigh<T>(s0, c, st, p0);
-        interleave<STEPS, 56 / STEPS, 16 / STEPS>();
-        keep_here(p0, sum);
-        st.l += sum;
-      }
-      if constexpr (TURNS) {
-        if (more) {
-          store_keys(buf ^ 1, in);
-          fetch_values(t + 1, page, in);
-          page = pages_of(t + 2);
-        }
-      }
-      if (wave_live) {
-        if (!open) cut_scores(s1, (uint32_t)(seen >> 32));
-        float top = row_top(s1, c), alpha = 1.0f;
-        const bool moved = must_move(top, st);
-        if (moved) alpha = move_bound(top, st);
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-          for (int d = 0; d < DT; ++d) o[d] = T::mfma(vt[2 * s * D + d * 32], p0[s], o[d]);
-        float sum = weigh<T>(s1, c, st, p1);
-        interleave<2 * DT, 56 / (2 * DT), 16 / (2 * DT)>();
-        keep_here(p1, sum);
-        if (moved) rescale(alpha);                           // the first block was weighed with the earlier bound
-        st.l += sum;
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-          for (int d = 0; d < DT; ++d) o[d] = T::mfma(vt[(4 + 2 * s) * D + d * 32], p1[s], o[d]);
-        interleave<2 * DT, 0, 0>();
-        settle(o);
-        if (s_bad[buf] == t) {
-          add_nonfinite<T, D, TREE>(a.v + head_at, e.pages, a.pages, page_elems, a.page_log2, mask, kb, KT, o);
-          settle(o);
-        }
-      }
-      if (more) {
-        if constexpr (TURNS) {
-          store_values(buf ^ 1, t + 1, in);
+      auto stage = [&](int i) __attribute__((always_inline)) {
+        if (i < PER) {
+          lds[(buf ^ 1) * 2 * GRAN + i * THREADS + tid] = in_k[i];
+          load_keys(kp, i);
         } else {
-          store_keys(buf ^ 1, in);
-          store_values(buf ^ 1, t + 1, in_v);
+          lds[(buf * 2 + 1) * GRAN + (i - PER) * THREADS + tid] = in_v[i - PER];
+          load_values(vp, i - PER);
+        }
+      };
+      if (!has_rows) {
+        if constexpr (!LAST) {
+#pragma unroll
+          for (int i = 0; i < 2 * PER; ++i) stage(i);
+        }
+      } else {
+        // The period's matrix instructions in order, in quarters: scores of
+        // this tile's first block, product of the first block before, scores
+        // of the second block, product of the second block before.  A slot is
+        // one of them, the operand read AHEAD slots later, and its share of
+        // what else the quarter has to do.  The order is pinned: left to
+        // itself every read is waited for where it stands.
+        constexpr int N = STEPS, TOTAL = FIRST || LAST ? 2 * N : 4 * N, AHEAD = D == 256 ? 6 : 4;
+        auto quarter = [](int j) { return FIRST ? j / N * 2 : LAST ? j / N * 2 + 1 : j / N; };
+        auto read = [&](int j) __attribute__((always_inline)) {
+          const int at = quarter(j), i = j % N, x = (at >> 1) * 32;
+          return at & 1 ? vt[((at >> 1) * 4 + 2 * (i / DT)) * D + i % DT * 32] : kt[2 * i * KT + x];
+        };
+        u32x4v f[AHEAD];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) f[j] = read(j);
+        auto run = [&](auto which, auto&& extra) __attribute__((always_inline)) {
+          constexpr int Q = decltype(which)::value, FROM = (FIRST || LAST ? Q / 2 : Q) * N;
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int j = FROM + i;
+            u32x4v& operand = f[j % AHEAD];
+            if (Q == 0) sa = T::mfma(operand, q[i], sa);
+            if (Q == 1) o[i % DT] = T::mfma(operand, pa[i / DT], o[i % DT]);
+            if (Q == 2) sb = T::mfma(operand, q[i], sb);
+            if (Q == 3) o[i % DT] = T::mfma(operand, pb[i / DT], o[i % DT]);
+            if (j + AHEAD < TOTAL) operand = read(j + AHEAD);
+            extra(i);
+            if constexpr (!LAST) {
+              // the moves of this quarter (two quarters where the others are left out)
+              constexpr int M0 = (FIRST ? Q / 2 * 2 : Q) * PER / 2, M1 = (FIRST ? Q / 2 * 2 + 2 : Q + 1) * PER / 2;
+#pragma unroll
+              for (int m = M0 + i * (M1 - M0) / N; m < M0 + (i + 1) * (M1 - M0) / N; ++m) stage(m);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        };
+        constexpr std::integral_constant<int, 0> Q0{};
+        constexpr std::integral_constant<int, 1> Q1{};
+        constexpr std::integral_constant<int, 2> Q2{};
+        constexpr std::integral_constant<int, 3> Q3{};
+        float top = -INFINITY, alpha = 1.0f, sum = 0.0f;
+        bool moved = false;
+        // the row maximum of a block, done after half a quarter
+        auto maximum = [&](const f32x16& s, int i) __attribute__((always_inline)) {
+          constexpr int E = 32 / N;
+          if (i < N / 2) {
+#pragma unroll
+            for (int e = i * E; e < (i + 1) * E; e += 2) top = fmaxf(top, fmaxf(s[e], s[e + 1]));
+          } else if (i == N / 2) {
+            top = max_of_halves(top) * c;
+          }
+        };
+        auto weights = [&](const f32x16& s, u32x4v (&p)[2], int i) __attribute__((always_inline)) {
+          constexpr int E = 16 / N;
+#pragma unroll
+          for (int e = i * E; e < (i + 1) * E; ++e) weigh_one<T>(s, c, st, e, sum, p);
+        };
+        if (!FIRST && !open) cut_scores(sb, seen_b);
+        if constexpr (!LAST) {
+          sa = f32x16{};
+          if constexpr (FIRST)
+            run(Q0, [](int) {});
+          else
+            run(Q0, [&](int i) __attribute__((always_inline)) { maximum(sb, i); });
+        } else {
+          top = row_top(sb, c);
+        }
+        if constexpr (!FIRST) {
+          moved = must_move(top, st);
+          if (moved) alpha = move_bound(top, st);
+          run(Q1, [&](int i) __attribute__((always_inline)) { weights(sb, pb, i); });
+          keep_here(pb, sum);
+          if (moved) rescale(alpha);                         // what went before was weighed with the earlier bound
+          st.l += sum;
+        }
+        if constexpr (!LAST) {
+          open = seen_by_wave.tile(kb, KT);
+          if (!open) {
+            const uint64_t seen = mask.template bits<TREE>(kb);
+            cut_scores(sa, (uint32_t)seen);
+            seen_b = (uint32_t)(seen >> 32);
+          }
+          sb = f32x16{};
+          top = -INFINITY;
+          alpha = 1.0f;
+          sum = 0.0f;
+          run(Q2, [&](int i) __attribute__((always_inline)) { maximum(sa, i); });
+          moved = must_move(top, st);
+          if (moved) alpha = move_bound(top, st);
+        }
+        if constexpr (FIRST) {
+          sum = weigh<T>(sa, c, st, pa);
+        } else if constexpr (LAST) {
+          run(Q3, [](int) {});
+        } else {
+          run(Q3, [&](int i) __attribute__((always_inline)) { weights(sa, pa, i); });
+        }
+        if constexpr (!LAST) {
+          keep_here(pa, sum);
+          if (!FIRST && moved) rescale(alpha);
+          st.l += sum;
+        }
+        settle(o);
+        if constexpr (!FIRST) {
+          if (s_bad[buf ^ 1] == t - 1) {
+            add_nonfinite<T, D, TREE>(a.v + head_at, e.pages, a.pages, page_elems, a.page_log2, mask,
+                                      list.key<KT>(t - 1), KT, o);
+            settle(o);
+          }
         }
       }
       lds_barrier();
+      // A tile that some row does not see in full has its values cleaned in
+      // place before they are used; s_bad: the last tile where that changed any.
+      if constexpr (!LAST) {
+        if (!seen_by_all.tile(kb, KT)) {
+          u32x4v v[PER];
+          u32x4v* own = lds + (buf * 2 + 1) * GRAN + tid;
+#pragma unroll
+          for (int n = 0; n < PER; ++n) v[n] = own[n * THREADS];
+          if (drop_nonfinite<T>(v)) s_bad[buf] = t;
+#pragma unroll
+          for (int n = 0; n < PER; ++n) own[n * THREADS] = v[n];
+          lds_barrier();
+        }
+      }
+    };
+    if (t0 < t1) {
+      constexpr std::true_type yes{};
+      constexpr std::false_type no{};
+      period(t0, yes, no);
+      for (int t = t0 + 1; t < t1; ++t) period(t, no, no);
+      period(t1, no, yes);
     }
 
     settle(o);
@@ -949,9 +1025,16 @@ hipError_t launch_typed(AttnArgs& a, hipStream_t stream) {
     return hipGetLastError();
   }
   constexpr size_t lds = 2 * 2 * (size_t)kManyKeys * D * 2;
-  static hipError_t ready = hipFuncSetAttribute((const void*)&attention_many_kernel<T, D, TREE>,
-                                                hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-  if (ready != hipSuccess) return ready;
+  static uint64_t lds_attr = 0;                // devices whose dynamic LDS limit is raised
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return hipErrorInvalidDevice;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(lds_attr & bit)) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&attention_many_kernel<T, D, TREE>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+    lds_attr |= bit;
+  }
   a.target = many_target(a);
   a.rounds = rounds_of(a, a.target);
   attention_many_kernel<T, D, TREE><<<(unsigned)(a.target * a.heads_kv), Many<D>::kThreads, lds, stream>>>(a);

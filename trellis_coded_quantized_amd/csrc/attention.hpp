@@ -169,22 +169,12 @@ struct OpenKeys {
   __device__ __forceinline__ bool tile(int kb, int keys) const {
     return kb + keys <= to && (kb >= from || kb + keys <= sinks);
   }
-  __device__ __forceinline__ bool touches(int kb, int keys) const {
-    return kb < to && (kb + keys > from || kb < sinks);
-  }
 };
 
 template <bool TREE>
 __device__ __forceinline__ OpenKeys open_keys(const AttnArgs& a, const Entry& e, int i0, int i1) {
   if (TREE) return {0, e.ctx, 0};
   return {a.window > 0 ? max(e.ctx + i1 - a.window + 1, 0) : 0, min(e.ctx + i0 + 1, e.total), a.sinks};
-}
-
-// The keys that any row of tokens i0 .. i1 may see.
-template <bool TREE>
-__device__ __forceinline__ OpenKeys reach_keys(const AttnArgs& a, const Entry& e, int i0, int i1) {
-  if (TREE) return {0, e.total, 0};
-  return {a.window > 0 ? max(e.ctx + i0 - a.window + 1, 0) : 0, min(e.ctx + i1 + 1, e.total), a.sinks};
 }
 
 // x and the same of the lane 32 away, the larger of the two.
@@ -242,6 +232,18 @@ __device__ __forceinline__ float weigh(const f32x16& s, float c, const Running& 
       p[h][w] = T::pack(x, y);
     }
   return sum[0] + sum[1];
+}
+
+// The same one score at a time, e = 0 .. 15 in order: a pair is packed with its
+// second one.
+template <typename T>
+__device__ __forceinline__ void weigh_one(const f32x16& s, float c, const Running& st, int e, float& sum,
+                                          u32x4v (&p)[2]) {
+  const float bound = st.m == -INFINITY ? 0.0f : st.m;
+  const float x = __builtin_amdgcn_exp2f(fmaf(s[e], c, -bound));
+  sum += x;
+  const int h = e >> 3, w = (e >> 1) & 3;
+  p[h][w] = e & 1 ? T::pack(__builtin_bit_cast(float, (uint32_t)p[h][w]), x) : __builtin_bit_cast(uint32_t, x);
 }
 
 // At D = 256 a wave's outputs stay in accumulation registers; left alone, the
