@@ -866,68 +866,61 @@ __global__ __launch_bounds__(Many<D>::kThreads) void attention_many_kernel(AttnA
 
     settle(o);
     const float l = st.l + __shfl_xor(st.l, 32);
-    int local = wave * 32 + col;
-    asm volatile("" : "+v"(local));          // the row's numbers are worked out again, not kept through the loop
-    if (r0 + local >= rows) continue;
-    if (whole) {
-      const int i = (r0 + local) / group, hq = h * group + (r0 + local) % group;
+    // Outputs of whole units go through LDS, where a wave's rows lie as they do
+    // in memory (granules of 16 bytes, turned by the row against bank
+    // conflicts), and leave as whole rows.  Parts are only read by the fold:
+    // they lie as the registers do, a wave's 64 lanes side by side.
+    int olane = lane;
+    asm volatile("" : "+v"(olane));          // the lane's addresses are worked out here, not kept through the loop
+    const int ocol = olane & 31, ohalf = olane >> 5;
+    if (has_rows && whole) {
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      uint16_t* dst = a.out + ((int64_t)(e.first + i) * a.heads_q + hq) * D + 4 * half;
+      constexpr int GRANS = D / 8;
+      uint16_t* tile = reinterpret_cast<uint16_t*>(lds) + wave * 32 * D;
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<u32x2v*>(dst + d * 32 + 8 * j) =
+          *reinterpret_cast<u32x2v*>(tile + ocol * D + ((d * 4 + j) ^ (ocol & 7)) * 8 + ohalf * 4) =
               u32x2v{T::pack(o[d][4 * j] * inv, o[d][4 * j + 1] * inv), T::pack(o[d][4 * j + 2] * inv, o[d][4 * j + 3] * inv)};
-      continue;
+#pragma unroll
+      for (int n = 0; n < GRANS / 2; ++n) {
+        const int r = (n * 64 + olane) / GRANS, g = (n * 64 + olane) % GRANS, at = w0 + r;
+        const u32x4v x = *reinterpret_cast<const u32x4v*>(tile + r * D + (g ^ (r & 7)) * 8);
+        const int i = at / group;
+        if (at < rows)
+          *reinterpret_cast<u32x4v*>(a.out + ((int64_t)(e.first + i) * a.heads_q + h * group + at - i * group) * D + g * 8) = x;
+      }
+    } else if (has_rows) {
+      const int64_t slot = (slot_at * a.heads_kv + h) * ROWS + wave * 32;
+      if (ohalf == 0) *reinterpret_cast<f32x2p*>(a.part_ml + (slot + ocol) * 2) = f32x2p{st.m, l};
+      float* part = a.part_o + slot * D + olane * 4;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<f32x4v*>(part + (d * 4 + j) * 256) =
+              f32x4v{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
     }
-    const int64_t slot = (slot_at * a.heads_kv + h) * ROWS + local;
-    if (half == 0) *reinterpret_cast<f32x2p*>(a.part_ml + slot * 2) = f32x2p{st.m, l};
-    if (st.m == -INFINITY) continue;
-    float* part = a.part_o + slot * D + 4 * half;
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<f32x4v*>(part + d * 32 + 8 * j) =
-            f32x4v{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
+    lds_barrier();                                           // the next segment's tiles take the same place
   }
 }
 
 // ---- fold ----------------------------------------------------------------
 // o = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s over the parts s of a row.
 
-// D / 4 lanes take a row's dimensions, and read its (m, l) pairs side by side.
-// The note of the unit says where its parts are.
-//   few rows:   notes by entry; parts are consecutive slots of 32 rows a head.
-//     One row a workgroup, its 1024 / D groups of lanes take the parts in turn.
-//   many rows, trees: notes by the slot of the first part, parts every `step` slots.
-//   many rows, consecutive tokens: notes by the run that begins the unit; the
-//     first part is in place 0 or 1 of that run, the others in place 0 of the
-//     runs after it.  1024 / D rows a workgroup for both.  Notes are the slowest
-//     dimension of the grid: most of a short call's are empty, and as the
-//     fastest they left its work to one XCD (one tree of 64 tokens, 4096 keys,
-//     32 / 8 heads of 128: 34 us).
-enum FoldKind { kFoldFew, kFoldTree, kFoldRuns };
-
-template <typename T, int D, FoldKind KIND>
-__global__ __launch_bounds__(kThreads) void attention_fold_kernel(AttnArgs a) {
-  constexpr bool FEW = KIND == kFoldFew;
-  constexpr int LANES = D / 4, GROUPS = kThreads / LANES, SLOT = FEW ? kFewRows : Many<D>::kRows, BATCH = 8;
-  const int at_note = FEW ? blockIdx.x : blockIdx.z;
-  const PartNote note = a.part_note[at_note];
+// Few rows: notes by entry; parts are consecutive slots of 32 rows a head.  One
+// row a workgroup; D / 4 lanes take its dimensions and read its (m, l) pairs
+// side by side, and the 1024 / D groups of lanes take the parts in turn.
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads) void attention_fold_few_kernel(AttnArgs a) {
+  constexpr int LANES = D / 4, GROUPS = kThreads / LANES, BATCH = 8;
+  const PartNote note = a.part_note[blockIdx.x];
   if (note.parts == 0) return;
   const int gl = threadIdx.x % LANES, g = threadIdx.x / LANES, d = gl * 4;
-  const int h = FEW ? blockIdx.z : blockIdx.y, group = a.heads_q / a.heads_kv;
-  const int local = FEW ? blockIdx.y : blockIdx.x * GROUPS + g;
-  const int row = FEW ? local : (KIND == kFoldRuns ? note.place >> 1 : note.place) * SLOT + local;
-  if (row >= note.rows) return;                              // FEW: the whole workgroup
-  auto slot = [&](int s) -> int64_t {
-    const int64_t at = FEW                 ? note.place + s
-                       : KIND == kFoldTree ? (int64_t)at_note + (int64_t)s * note.step
-                                           : ((int64_t)at_note + s) * 2 + (s ? 0 : note.place & 1);
-    return (at * a.heads_kv + h) * SLOT + local;
-  };
+  const int h = blockIdx.z, group = a.heads_q / a.heads_kv, row = blockIdx.y;
+  if (row >= note.rows) return;
+  auto slot = [&](int s) -> int64_t { return ((int64_t)(note.place + s) * a.heads_kv + h) * kFewRows + row; };
   float top = -INFINITY;
   for (int s = gl; s < note.parts; s += LANES) top = fmaxf(top, a.part_ml[slot(s) * 2]);
 #pragma unroll
@@ -943,7 +936,7 @@ __global__ __launch_bounds__(kThreads) void attention_fold_kernel(AttnArgs a) {
         sum += f * ml[1];
       }
       const int n = min(LANES, note.parts - base);
-      for (int s0 = FEW ? g * BATCH : 0; s0 < n; s0 += FEW ? GROUPS * BATCH : BATCH) {
+      for (int s0 = g * BATCH; s0 < n; s0 += GROUPS * BATCH) {
         f32x4v x[BATCH];
 #pragma unroll
         for (int k = 0; k < BATCH; ++k)
@@ -960,16 +953,79 @@ __global__ __launch_bounds__(kThreads) void attention_fold_kernel(AttnArgs a) {
 #pragma unroll
     for (int x = LANES / 2; x; x >>= 1) sum += __shfl_xor(sum, x);
   }
-  if (FEW) {
-    __shared__ f32x4v s_acc[kThreads];
-    s_acc[threadIdx.x] = acc;
-    __syncthreads();
-    if (g) return;
-    for (int o = 1; o < GROUPS; ++o) acc += s_acc[o * LANES + gl];
-  }
+  __shared__ f32x4v s_acc[kThreads];
+  s_acc[threadIdx.x] = acc;
+  __syncthreads();
+  if (g) return;
+  for (int o = 1; o < GROUPS; ++o) acc += s_acc[o * LANES + gl];
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   uint16_t* dst = a.out + ((int64_t)(note.first + row / group) * a.heads_q + h * group + row % group) * D + d;
   *reinterpret_cast<u32x2v*>(dst) = u32x2v{T::pack(acc[0] * inv, acc[1] * inv), T::pack(acc[2] * inv, acc[3] * inv)};
+}
+
+// Many rows, trees: notes by the slot of the first part, parts every `step`
+// slots.  Consecutive tokens: notes by the run that begins the unit; the first
+// part is in place 0 or 1 of that run, the others in place 0 of the runs after
+// it.  A wave takes 32 rows and one granule of 8 dimensions, as its lanes lie
+// in the parts; the workgroup's four granules leave together.  Notes are the
+// slowest dimension of the grid: most of a short call's are empty, and as the
+// fastest they left its work to one XCD (one tree of 64 tokens, 4096 keys,
+// 32 / 8 heads of 128: 34 us).
+template <typename T, int D, bool TREE>
+__global__ __launch_bounds__(kThreads) void attention_fold_many_kernel(AttnArgs a) {
+  constexpr int ROWS = Many<D>::kRows, BATCH = 8;
+  const PartNote note = a.part_note[blockIdx.z];
+  if (note.parts == 0) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 31, half = lane >> 5;
+  const int h = blockIdx.y, group = a.heads_q / a.heads_kv;
+  const int block = blockIdx.x / (D / 32), gran = blockIdx.x % (D / 32) * 4 + wave;
+  const int r0 = (TREE ? note.place : note.place >> 1) * ROWS + block * 32;
+  if (r0 >= note.rows) return;
+  auto slot = [&](int s) -> int64_t {
+    const int64_t at = TREE ? (int64_t)blockIdx.z + (int64_t)s * note.step
+                            : ((int64_t)blockIdx.z + s) * 2 + (s ? 0 : note.place & 1);
+    return (at * a.heads_kv + h) * ROWS + block * 32;
+  };
+  f32x4v acc = {};
+  float top = -INFINITY, sum = 0.0f;
+  const bool live = r0 + col < note.rows;                    // rows past the end were not written
+  for (int s0 = 0; s0 < note.parts; s0 += BATCH) {
+    f32x2p ml[BATCH];
+    f32x4v x[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int64_t at = slot(min(s0 + k, note.parts - 1));
+      ml[k] = *reinterpret_cast<const f32x2p*>(a.part_ml + (at + col) * 2);
+      x[k] = *reinterpret_cast<const f32x4v*>(a.part_o + at * D + gran * 256 + lane * 4);
+    }
+    float up = top;
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) up = fmaxf(up, s0 + k < note.parts ? ml[k][0] : -INFINITY);
+    const float down = up == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(top - up);
+    top = up;
+    sum *= down;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[v] *= down;
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      // a part that saw no key has nothing but zeros
+      const bool none = !(s0 + k < note.parts) || ml[k][0] == -INFINITY;
+      const float f = none ? 0.0f : __builtin_amdgcn_exp2f(ml[k][0] - up);
+      sum += none ? 0.0f : f * ml[k][1];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[v] += none ? 0.0f : f * x[k][v];
+    }
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  __shared__ u32x2v s_out[32][8 + 1];
+  if (live)
+    s_out[col][wave * 2 + half] =
+        u32x2v{T::pack(acc[0] * inv, acc[1] * inv), T::pack(acc[2] * inv, acc[3] * inv)};
+  __syncthreads();
+  const int r = tid >> 3, g = tid & 7, i = (r0 + r) / group;
+  if (r0 + r < note.rows)
+    *reinterpret_cast<u32x2v*>(a.out + ((int64_t)(note.first + i) * a.heads_q + h * group + r0 + r - i * group) * D +
+                               blockIdx.x % (D / 32) * 32 + g * 4) = s_out[r][g];
 }
 
 bool few_rows(const AttnArgs& a) { return (int64_t)a.max_q * (a.heads_q / a.heads_kv) <= kFewRows; }
@@ -1021,7 +1077,7 @@ hipError_t launch_typed(AttnArgs& a, hipStream_t stream) {
     a.rounds = rounds_of(a, a.target);
     const unsigned slots = (unsigned)few_slots(a), rows = (unsigned)(a.max_q * (a.heads_q / a.heads_kv));
     attention_few_kernel<T, D, TREE><<<dim3(slots, a.heads_kv), kThreads, 0, stream>>>(a);
-    attention_fold_kernel<T, D, kFoldFew><<<dim3(a.entries, rows, a.heads_kv), kThreads, 0, stream>>>(a);
+    attention_fold_few_kernel<T, D><<<dim3(a.entries, rows, a.heads_kv), kThreads, 0, stream>>>(a);
     return hipGetLastError();
   }
   constexpr size_t lds = 2 * 2 * (size_t)kManyKeys * D * 2;
@@ -1039,8 +1095,7 @@ hipError_t launch_typed(AttnArgs& a, hipStream_t stream) {
   a.rounds = rounds_of(a, a.target);
   attention_many_kernel<T, D, TREE><<<(unsigned)(a.target * a.heads_kv), Many<D>::kThreads, lds, stream>>>(a);
   const unsigned notes = (unsigned)(TREE ? a.target * a.rounds : a.target);
-  attention_fold_kernel<T, D, TREE ? kFoldTree : kFoldRuns>
-      <<<dim3(Many<D>::kRows * D / (4 * kThreads), a.heads_kv, notes), kThreads, 0, stream>>>(a);
+  attention_fold_many_kernel<T, D, TREE><<<dim3(Many<D>::kRows * D / (4 * kThreads), a.heads_kv, notes), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
