@@ -936,14 +936,18 @@ __global__ __launch_bounds__(kThreads) void attention_fold_few_kernel(AttnArgs a
         sum += f * ml[1];
       }
       const int n = min(LANES, note.parts - base);
-      for (int s0 = g * BATCH; s0 < n; s0 += GROUPS * BATCH) {
+      for (int s0 = 0; s0 < n; s0 += GROUPS * BATCH) {
         f32x4v x[BATCH];
 #pragma unroll
-        for (int k = 0; k < BATCH; ++k)
-          x[k] = *reinterpret_cast<const f32x4v*>(a.part_o + slot(base + min(s0 + k, n - 1)) * D + d);
+        for (int k = 0; k < BATCH; ++k) {
+          const int s = s0 + k * GROUPS + g;
+          x[k] = f32x4v{};
+          if (s < n) x[k] = *reinterpret_cast<const f32x4v*>(a.part_o + slot(base + s) * D + d);
+        }
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
-          const float fs = s0 + k < n ? __shfl(f, (s0 + k) % LANES, LANES) : 0.0f;
+          const int s = s0 + k * GROUPS + g;
+          const float got = __shfl(f, s % LANES, LANES), fs = s < n ? got : 0.0f;
           // a part that saw no key left its outputs unwritten
 #pragma unroll
           for (int v = 0; v < 4; ++v) acc[v] += fs != 0.0f ? fs * x[k][v] : 0.0f;
@@ -994,13 +998,16 @@ __global__ __launch_bounds__(kThreads) void attention_fold_many_kernel(AttnArgs 
     f32x4v x[BATCH];
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
-      const int64_t at = slot(min(s0 + k, note.parts - 1));
+      ml[k] = f32x2p{-INFINITY, 0.0f};
+      x[k] = f32x4v{};
+      if (s0 + k >= note.parts) continue;
+      const int64_t at = slot(s0 + k);
       ml[k] = *reinterpret_cast<const f32x2p*>(a.part_ml + (at + col) * 2);
       x[k] = *reinterpret_cast<const f32x4v*>(a.part_o + at * D + gran * 256 + lane * 4);
     }
     float up = top;
 #pragma unroll
-    for (int k = 0; k < BATCH; ++k) up = fmaxf(up, s0 + k < note.parts ? ml[k][0] : -INFINITY);
+    for (int k = 0; k < BATCH; ++k) up = fmaxf(up, ml[k][0]);
     const float down = up == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(top - up);
     top = up;
     sum *= down;
@@ -1009,11 +1016,10 @@ __global__ __launch_bounds__(kThreads) void attention_fold_many_kernel(AttnArgs 
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
       // a part that saw no key has nothing but zeros
-      const bool none = !(s0 + k < note.parts) || ml[k][0] == -INFINITY;
-      const float f = none ? 0.0f : __builtin_amdgcn_exp2f(ml[k][0] - up);
-      sum += none ? 0.0f : f * ml[k][1];
+      const float f = ml[k][0] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml[k][0] - up);
+      sum += f * ml[k][1];
 #pragma unroll
-      for (int v = 0; v < 4; ++v) acc[v] += none ? 0.0f : f * x[k][v];
+      for (int v = 0; v < 4; ++v) acc[v] += f * x[k][v];
     }
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
