@@ -328,7 +328,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_few_kern
 // innermost), 32 a wave, and walks its keys in tiles of 64 that all waves
 // share through LDS, in the cache's own granule order, so LDS reads are
 // contiguous across lanes and nothing is transposed.  At D = 256 a wave's
-// outputs and queries fill a SIMD's registers alone, and it is 128 rows.
+// outputs and queries fill a SIMD's registers alone, and it is 128 rows, as
+// where no entry has more.
 //
 // A tile is two blocks of 32 keys.  The product with the values runs one tile
 // behind the scores: a block's maximum is taken under the next block's scores,
@@ -339,12 +340,20 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_few_kern
 // before its use; hints to the scheduler left most reads waited for at once
 // (2048 tokens, 18432 keys, 24 / 4 heads of 256: 644 TFLOP/s against 889;
 // 32 / 8 heads of 128: 906 against 985).  Two workgroups of 128 rows a compute
-// unit were slower than one of 256.
-template <int D>
+// unit were slower than one of 256 where both are full.
+template <int W>
 struct Many {
-  static constexpr int kWaves = D == 256 ? 4 : 8;
-  static constexpr int kThreads = 64 * kWaves, kRows = 32 * kWaves;
+  static constexpr int kThreads = 64 * W, kRows = 32 * W;
 };
+// Waves of a workgroup, by the rows that an entry can have.  Where 128 rows do,
+// two workgroups of four waves have twice the loads under way on a compute
+// unit: 64 trees of 16 tokens over 4096 keys, 32 / 8 heads of 128, 240 us
+// against 300 (heads of 64: 148 against 219).  A single entry loses to
+// the doubled parts (32 tokens over 30000 keys: 44 us against 41).
+constexpr int64_t kHalfRows = 128;
+inline int many_waves(const AttnArgs& a) {
+  return a.head_dim == 256 || (int64_t)a.max_q * (a.heads_q / a.heads_kv) <= kHalfRows ? 4 : 8;
+}
 
 // Weights that were taken before this point, not where they are used.
 __device__ __forceinline__ void keep_here(u32x4v (&p)[2], float& sum) {
@@ -518,10 +527,10 @@ __device__ __forceinline__ Slot find_slot(const AttnArgs& a, const int (&tiles0)
   return s;
 }
 
-template <typename T, int D, bool TREE>
-__global__ __launch_bounds__(Many<D>::kThreads) void attention_many_kernel(AttnArgs a) {
-  constexpr int STEPS = D / 16, DT = D / 32, KT = kManyKeys, WAVES = Many<D>::kWaves, THREADS = Many<D>::kThreads;
-  constexpr int ROWS = Many<D>::kRows;
+template <typename T, int D, int WAVES, bool TREE>
+__global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attention_many_kernel(AttnArgs a) {
+  constexpr int STEPS = D / 16, DT = D / 32, KT = kManyKeys, THREADS = Many<WAVES>::kThreads;
+  constexpr int ROWS = Many<WAVES>::kRows;
   constexpr int GRAN = KT * D / 8;                           // granules of one operand's tile
   constexpr int PER = GRAN / THREADS;
   extern __shared__ __align__(16) u32x4v lds[];              // [2][keys, values][GRAN]
@@ -975,9 +984,9 @@ __global__ __launch_bounds__(kThreads) void attention_fold_few_kernel(AttnArgs a
 // slowest dimension of the grid: most of a short call's are empty, and as the
 // fastest they left its work to one XCD (one tree of 64 tokens, 4096 keys,
 // 32 / 8 heads of 128: 34 us).
-template <typename T, int D, bool TREE>
+template <typename T, int D, int WAVES, bool TREE>
 __global__ __launch_bounds__(kThreads) void attention_fold_many_kernel(AttnArgs a) {
-  constexpr int ROWS = Many<D>::kRows, BATCH = 8;
+  constexpr int ROWS = Many<WAVES>::kRows, BATCH = 8;
   const PartNote note = a.part_note[blockIdx.z];
   if (note.parts == 0) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 31, half = lane >> 5;
@@ -1050,11 +1059,13 @@ int64_t few_slots(const AttnArgs& a) {
   return slots > a.entries ? slots : a.entries;
 }
 
-// Runs per key head of the many-row kernel: one workgroup a compute unit, over
-// the heads.  (At D = 64 two would fit the LDS but not the registers; cut for
-// two, 64 tokens over 30000 keys, 32 / 8 heads, took 56 us against 44.)
+// Runs per key head of the many-row kernel: the workgroups that run at once,
+// over the heads.  (At D = 64 two of eight waves would fit the LDS but not the
+// registers; cut for two, 64 tokens over 30000 keys, 32 / 8 heads, took 56 us
+// against 44.)
 int many_target(const AttnArgs& a) {
-  return device_cus() / a.heads_kv > 1 ? device_cus() / a.heads_kv : 1;
+  const int resident = device_cus() * (a.head_dim != 256 && many_waves(a) == 4 ? 2 : 1);
+  return resident / a.heads_kv > 1 ? resident / a.heads_kv : 1;
 }
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
@@ -1069,12 +1080,33 @@ Parts part_bytes(const AttnArgs& a) {
     slots = few_slots(a);
     rows = slots * kFewRows;
   } else {
-    const int64_t of_slot = a.head_dim == 256 ? Many<256>::kRows : Many<128>::kRows;
+    const int64_t of_slot = 32 * many_waves(a);
     slots = (int64_t)many_target(a) * (a.tree ? rounds_of(a, many_target(a)) : 1);
     rows = slots * (a.tree ? 1 : 2) * of_slot;
   }
   rows *= a.heads_kv;
   return {round256((size_t)rows * a.head_dim * 4), round256((size_t)rows * 8), round256((size_t)slots * sizeof(PartNote))};
+}
+
+template <typename T, int D, int WAVES, bool TREE>
+hipError_t launch_many(AttnArgs& a, hipStream_t stream) {
+  constexpr size_t lds = 2 * 2 * (size_t)kManyKeys * D * 2;
+  static uint64_t lds_attr = 0;                // devices whose dynamic LDS limit is raised
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return hipErrorInvalidDevice;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(lds_attr & bit)) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&attention_many_kernel<T, D, WAVES, TREE>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+    lds_attr |= bit;
+  }
+  a.target = many_target(a);
+  a.rounds = rounds_of(a, a.target);
+  attention_many_kernel<T, D, WAVES, TREE><<<(unsigned)(a.target * a.heads_kv), Many<WAVES>::kThreads, lds, stream>>>(a);
+  const unsigned notes = (unsigned)(TREE ? a.target * a.rounds : a.target);
+  attention_fold_many_kernel<T, D, WAVES, TREE><<<dim3(Many<WAVES>::kRows * D / (4 * kThreads), a.heads_kv, notes), kThreads, 0, stream>>>(a);
+  return hipGetLastError();
 }
 
 template <typename T, int D, bool TREE>
@@ -1087,23 +1119,9 @@ hipError_t launch_typed(AttnArgs& a, hipStream_t stream) {
     attention_fold_few_kernel<T, D><<<dim3(a.entries, rows, a.heads_kv), kThreads, 0, stream>>>(a);
     return hipGetLastError();
   }
-  constexpr size_t lds = 2 * 2 * (size_t)kManyKeys * D * 2;
-  static uint64_t lds_attr = 0;                // devices whose dynamic LDS limit is raised
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return hipErrorInvalidDevice;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (!(lds_attr & bit)) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&attention_many_kernel<T, D, TREE>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (e != hipSuccess) return e;
-    lds_attr |= bit;
-  }
-  a.target = many_target(a);
-  a.rounds = rounds_of(a, a.target);
-  attention_many_kernel<T, D, TREE><<<(unsigned)(a.target * a.heads_kv), Many<D>::kThreads, lds, stream>>>(a);
-  const unsigned notes = (unsigned)(TREE ? a.target * a.rounds : a.target);
-  attention_fold_many_kernel<T, D, TREE><<<dim3(Many<D>::kRows * D / (4 * kThreads), a.heads_kv, notes), kThreads, 0, stream>>>(a);
-  return hipGetLastError();
+  if constexpr (D != 256)
+    if (many_waves(a) == 8) return launch_many<T, D, 8, TREE>(a, stream);
+  return launch_many<T, D, 4, TREE>(a, stream);
 }
 
 template <typename T, int D>
