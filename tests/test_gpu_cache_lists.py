@@ -51,3 +51,11 @@ def test_accept_lengths_of_many_sequences(in_place):
     assert torch.equal(w.v.view(torch.int16), v.view(torch.int16))
     if not in_place:
         assert w.lengths.tolist() == start
+
+
+def test_fork_that_takes_page_0_beside_a_parent_of_full_pages():
+    w = World(seqs=6, width=4, pages=12, layers=3)
+    w.reserve([0, 1, 2], [5, 33, 32])                        # page 0, pages 1 to 3, pages 4 and 5
+    w.free([0])
+    w.fork([1, 2, 1], [3, 4, 5])                             # copies into pages 0 and 6, nothing for the second
+    assert w.table[3].tolist()[2] == 0
