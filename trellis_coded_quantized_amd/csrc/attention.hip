@@ -264,7 +264,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_few_kern
     if (more) load_values(t + kWaves);
     settle(o);
     if (__any(bad)) {
-      add_nonfinite<T, D, TREE>(a.v + head_at, e.pages, a.pages, page_elems, a.page_log2, mask, kb, 32, o);
+      add_nonfinite<T, D, TREE>(a.v + head_at, e.pages, (int)a.width << a.page_log2, a.pages, page_elems, a.page_log2,
+                                mask, kb, 32, o);
       settle(o);
     }
   }
@@ -843,8 +844,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attention_many_k
         settle(o);
         if constexpr (!FIRST) {
           if (s_bad[buf ^ 1] == t - 1) {
-            add_nonfinite<T, D, TREE>(a.v + head_at, e.pages, a.pages, page_elems, a.page_log2, mask,
-                                      list.key<KT>(t - 1), KT, o);
+            add_nonfinite<T, D, TREE>(a.v + head_at, e.pages, (int)a.width << a.page_log2, a.pages, page_elems,
+                                      a.page_log2, mask, list.key<KT>(t - 1), KT, o);
             settle(o);
           }
         }

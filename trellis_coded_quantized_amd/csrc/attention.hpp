@@ -261,7 +261,8 @@ __device__ __forceinline__ void settle(f32x16 (&o)[DT]) {
 // was ever written.  In a tile that some row sees in part they therefore
 // enter the product as zeros (drop_nonfinite, which says whether there were
 // any), and rows that do see one get it back from here: each lane walks the
-// tile's keys and adds what its row sees to its own outputs.
+// tile's keys and adds what its row sees to its own outputs.  The walk ends
+// with the table's room: the last tile may reach past it.
 template <typename T, int N>
 __device__ __forceinline__ bool drop_nonfinite(u32x4v (&v)[N]) {
   // an exponent of all ones carries into the sign's place when its last bit is added
@@ -283,11 +284,12 @@ __device__ __forceinline__ bool drop_nonfinite(u32x4v (&v)[N]) {
 }
 
 template <typename T, int D, bool TREE>
-__device__ __forceinline__ void add_nonfinite(const uint16_t* v_head, GlobalInts pages, uint32_t pool,
+__device__ __forceinline__ void add_nonfinite(const uint16_t* v_head, GlobalInts pages, int room, uint32_t pool,
                                               uint32_t page_elems, int page_log2, const RowMask& mask, int kb, int keys,
                                               f32x16 (&o)[D / 32]) {
-  const int half = (int)__lane_id() >> 5;
-  for (int key = kb; key < kb + keys; ++key) {
+  const int half = (int)__lane_id() >> 5, n = min(keys, room - kb);
+  for (int j = 0; j < n; ++j) {
+    const int key = kb + j;
     const uint16_t* v = v_head + (uint64_t)page_in_pool(pages[key >> page_log2], pool) * page_elems +
                         ((key & ((1 << page_log2) - 1)) >> 3) * D * 8 + (key & 7);
     const uint32_t sees = (uint32_t)mask.bits<TREE>(key) & 1u;
