@@ -393,8 +393,9 @@ int trellis_probe_gateup_decode_free(const uint32_t* gcodes, const uint16_t* gsc
  *
  * Device-side contents are not seen by the host checks.  Every kernel bounds
  * what it reads there: rows and pages outside the arrays are never touched,
- * keys without storage are never seen, sequence numbers outside 0..seqs-1
- * are skipped.
+ * keys without storage (a table entry that is no page of the pool, whatever
+ * lengths says) are never seen, sequence numbers outside 0..seqs-1 are
+ * skipped.
  */
 #define TRELLIS_KV_BF16 0
 #define TRELLIS_KV_F16 1

@@ -182,10 +182,15 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_few_kern
     page[1] = e.pages[min((kb + 16) >> a.page_log2, (int)a.width - 1)];
   };
   uint64_t at[2];                                            // their elements in the pools
+  uint32_t held = 0;                                         // the tile's keys whose page is there
   auto locate = [&]() {
+    held = 0;
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-      at[s] = (uint64_t)page_in_pool(__builtin_amdgcn_readfirstlane(page[s]), a.pages) * page_elems + head_at;
+    for (int s = 0; s < 2; ++s) {
+      const int32_t own = __builtin_amdgcn_readfirstlane(page[s]);
+      held |= page_ok(own, a.pages) ? 0xFFFFu << (16 * s) : 0u;
+      at[s] = (uint64_t)page_in_pool(own, a.pages) * page_elems + head_at;
+    }
   };
   auto load_keys = [&](int t) {
     const int kb = list.key<32>(t);
@@ -231,6 +236,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_few_kern
   for (; t < t1; t += kWaves) {
     const int kb = list.key<32>(t);
     const bool more = t + kWaves < t1;
+    const uint32_t here = held;
     f32x16 sc = f32x16{};
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) sc = T::mfma(kf[s], q[s], sc);
@@ -240,8 +246,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_few_kern
       load_pages(t + 2 * kWaves);
     }
     bool bad = false;
-    if (!seen_by_all.tile(kb, 32)) {
-      cut_scores(sc, (uint32_t)mask.bits<TREE>(kb));
+    if (!seen_by_all.tile(kb, 32) || here != ~0u) {
+      cut_scores(sc, (uint32_t)mask.bits<TREE>(kb) & here);
       bad = drop_nonfinite<T>(vf[0]);
       bad |= drop_nonfinite<T>(vf[1]);
     }
@@ -682,10 +688,12 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attention_many_k
 
     if (tid < 2) s_bad[tid] = -1;
     int32_t page_v = 0, page_k = 0;                          // pages of the tiles that are loaded next
+    uint64_t held = 0;                                       // a tile's keys whose page is there
     if (t0 < t1) {
       const int32_t page = pages_of(t0), after = pages_of(t0 + 1);
       page_v = after;
       page_k = pages_of(t0 + 2);
+      held = __ballot(page_ok(page, a.pages));
       const uint16_t* kp = keys_at(t0, page);
 #pragma unroll
       for (int n = 0; n < PER; ++n) load_keys(kp, n);
@@ -717,7 +725,9 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attention_many_k
       // Past the end the last tile is read again.
       const uint16_t* kp = nullptr;
       uint64_t vp = 0;
+      const uint64_t here = held;
       if constexpr (!LAST) {
+        held = __ballot(page_ok(page_v, a.pages));
         kp = keys_at(t + 2, page_k);
         vp = values_at(t + 1, page_v);
         page_v = page_k;
@@ -815,9 +825,9 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attention_many_k
           st.l += sum;
         }
         if constexpr (!LAST) {
-          open = seen_by_wave.tile(kb, KT);
+          open = seen_by_wave.tile(kb, KT) && here == ~0ull;
           if (!open) {
-            const uint64_t seen = mask.template bits<TREE>(kb);
+            const uint64_t seen = mask.template bits<TREE>(kb) & here;
             cut_scores(sa, (uint32_t)seen);
             seen_b = (uint32_t)(seen >> 32);
           }
@@ -854,7 +864,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attention_many_k
       // A tile that some row does not see in full has its values cleaned in
       // place before they are used; s_bad: the last tile where that changed any.
       if constexpr (!LAST) {
-        if (!seen_by_all.tile(kb, KT)) {
+        if (!seen_by_all.tile(kb, KT) || here != ~0ull) {
           u32x4v v[PER];
           u32x4v* own = lds + (buf * 2 + 1) * GRAN + tid;
 #pragma unroll

@@ -43,7 +43,7 @@ __device__ __forceinline__ int tile_key_of_row(int R) {
 struct Entry {
   int first, n;        // rows of q
   int ctx;             // tokens cached before this call
-  int total;           // keys with storage: ctx + n, at most the table's
+  int total;           // keys with a place in the table: ctx + n, at most its room
   GlobalInts pages;
 };
 
@@ -110,7 +110,9 @@ __device__ __forceinline__ TileList tile_list(const AttnArgs& a, const Entry& e,
 }
 
 // What one row sees: keys below `below` that are at least `from` or below
-// `sinks`, and, in a tree, node bits from key `below` on.
+// `sinks`, and, in a tree, node bits from key `below` on.  Keys whose page is
+// not there are taken out by the kernels, a tile at a time: its pages are at
+// hand when it is read.
 struct RowMask {
   int below, from, sinks;
   uint64_t nodes;
@@ -162,8 +164,8 @@ __device__ __forceinline__ RowMask row_mask(const AttnArgs& a, const Entry& e, i
   return r;
 }
 
-// The keys that every row of tokens i0 .. i1 sees: from .. to - 1, and those
-// below sinks.
+// The keys that every row of tokens i0 .. i1 sees if they have a page: from ..
+// to - 1, and those below sinks.
 struct OpenKeys {
   int from, to, sinks;
   __device__ __forceinline__ bool tile(int kb, int keys) const {
@@ -262,7 +264,9 @@ __device__ __forceinline__ void settle(f32x16 (&o)[DT]) {
 // enter the product as zeros (drop_nonfinite, which says whether there were
 // any), and rows that do see one get it back from here: each lane walks the
 // tile's keys and adds what its row sees to its own outputs.  The walk ends
-// with the table's room: the last tile may reach past it.
+// with the table's room: the last tile may reach past it.  What the row sees is
+// worked out once for the tile: key by key it cost the kernels that call this
+// registers in their main loop (heads of 256, trees: 37 spilled against 8).
 template <typename T, int N>
 __device__ __forceinline__ bool drop_nonfinite(u32x4v (&v)[N]) {
   // an exponent of all ones carries into the sign's place when its last bit is added
@@ -288,11 +292,13 @@ __device__ __forceinline__ void add_nonfinite(const uint16_t* v_head, GlobalInts
                                               uint32_t page_elems, int page_log2, const RowMask& mask, int kb, int keys,
                                               f32x16 (&o)[D / 32]) {
   const int half = (int)__lane_id() >> 5, n = min(keys, room - kb);
-  for (int j = 0; j < n; ++j) {
+  uint64_t seen = mask.bits<TREE>(kb);
+  for (int j = 0; j < n; ++j, seen >>= 1) {
     const int key = kb + j;
-    const uint16_t* v = v_head + (uint64_t)page_in_pool(pages[key >> page_log2], pool) * page_elems +
+    const int32_t page = pages[key >> page_log2];
+    const uint16_t* v = v_head + (uint64_t)page_in_pool(page, pool) * page_elems +
                         ((key & ((1 << page_log2) - 1)) >> 3) * D * 8 + (key & 7);
-    const uint32_t sees = (uint32_t)mask.bits<TREE>(key) & 1u;
+    const uint32_t sees = (uint32_t)seen & (page_ok(page, pool) ? 1u : 0u);
 #pragma unroll
     for (int d = 0; d < D / 32; ++d) {
 #pragma unroll

@@ -54,8 +54,8 @@ struct F16 {
 };
 
 // A page number from a table, kept inside the pool: entries that hold no
-// page (-1) or a wrong one are read as page 0, and what is read there is
-// masked.  Writers test page_ok and leave such slots alone.
+// page (-1) or a wrong one are read as page 0.  What is read there is another
+// sequence's: readers cut it by page_ok, writers leave such slots alone.
 __device__ __forceinline__ uint32_t page_in_pool(int32_t page, uint32_t pages) {
   return (uint32_t)page < pages ? (uint32_t)page : 0u;
 }
