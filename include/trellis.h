@@ -456,7 +456,8 @@ int trellis_qk_norm_rope(const uint16_t* q, int64_t q_stride, const uint16_t* k,
  * ancestors[row] (a token that is to see itself has its own bit set); bits
  * without a token are ignored.  One token with mask 1 is plain decoding.  A
  * row that sees nothing gives zeros.  Infinities and NaN in tokens that a row
- * does not see do not reach it.
+ * does not see do not reach it; a NaN among the scores of those that it sees
+ * makes the row NaN, however long its context is.
  *   q [tokens, heads_q, head_dim], rows q_stride elements apart (a multiple of 8)
  *   q_start int32 [n+1] ascending;  ancestors int64 [tokens] (bit masks)
  *   max_q: the most tokens of any entry, 1..TRELLIS_TREE_MAX; rows past it

@@ -294,7 +294,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_few_kern
   for (int w = 1; w < kWaves; ++w) otop = fmaxf(otop, s_m[w][orow]);
 #pragma unroll
   for (int w = 0; w < kWaves; ++w)
-    osum += s_m[w][orow] == -INFINITY ? 0.0f : s_l[w][orow] * __builtin_amdgcn_exp2f(s_m[w][orow] - otop);
+    osum += s_l[w][orow] * (s_m[w][orow] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(s_m[w][orow] - otop));
   const bool whole = u.splits == 1;
   const float inv = whole ? (osum == 0.0f ? 0.0f : 1.0f / osum) : 1.0f;
   const int64_t slot = (int64_t)blockIdx.x * a.heads_kv + h;
@@ -928,6 +928,9 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attention_many_k
 
 // ---- fold ----------------------------------------------------------------
 // o = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s over the parts s of a row.
+// A part with m_s = -inf has a factor of zero, but is not left out: o_s and l_s
+// are zeros where the row sees no key of it, and NaN where every score that it
+// sees there is NaN (the maximum passes over those).
 
 // Few rows: notes by entry; parts are consecutive slots of 32 rows a head.  One
 // row a workgroup; D / 4 lanes take its dimensions and read its (m, l) pairs
@@ -947,36 +950,33 @@ __global__ __launch_bounds__(kThreads) void attention_fold_few_kernel(AttnArgs a
   for (int x = LANES / 2; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
   f32x4v acc = {};
   float sum = 0.0f;
-  if (top != -INFINITY) {
-    for (int base = 0; base < note.parts; base += LANES) {
-      float f = 0.0f;
-      if (base + gl < note.parts) {
-        const f32x2p ml = *reinterpret_cast<const f32x2p*>(a.part_ml + slot(base + gl) * 2);
-        f = ml[0] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml[0] - top);
-        sum += f * ml[1];
+  for (int base = 0; base < note.parts; base += LANES) {
+    float f = 0.0f;
+    if (base + gl < note.parts) {
+      const f32x2p ml = *reinterpret_cast<const f32x2p*>(a.part_ml + slot(base + gl) * 2);
+      f = ml[0] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml[0] - top);
+      sum += f * ml[1];
+    }
+    const int n = min(LANES, note.parts - base);
+    for (int s0 = 0; s0 < n; s0 += GROUPS * BATCH) {
+      f32x4v x[BATCH];
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        const int s = s0 + k * GROUPS + g;
+        x[k] = f32x4v{};
+        if (s < n) x[k] = *reinterpret_cast<const f32x4v*>(a.part_o + slot(base + s) * D + d);
       }
-      const int n = min(LANES, note.parts - base);
-      for (int s0 = 0; s0 < n; s0 += GROUPS * BATCH) {
-        f32x4v x[BATCH];
 #pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-          const int s = s0 + k * GROUPS + g;
-          x[k] = f32x4v{};
-          if (s < n) x[k] = *reinterpret_cast<const f32x4v*>(a.part_o + slot(base + s) * D + d);
-        }
+      for (int k = 0; k < BATCH; ++k) {
+        const int s = s0 + k * GROUPS + g;
+        const float got = __shfl(f, s % LANES, LANES), fs = s < n ? got : 0.0f;
 #pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-          const int s = s0 + k * GROUPS + g;
-          const float got = __shfl(f, s % LANES, LANES), fs = s < n ? got : 0.0f;
-          // a part that saw no key left its outputs unwritten
-#pragma unroll
-          for (int v = 0; v < 4; ++v) acc[v] += fs != 0.0f ? fs * x[k][v] : 0.0f;
-        }
+        for (int v = 0; v < 4; ++v) acc[v] += fs * x[k][v];
       }
     }
-#pragma unroll
-    for (int x = LANES / 2; x; x >>= 1) sum += __shfl_xor(sum, x);
   }
+#pragma unroll
+  for (int x = LANES / 2; x; x >>= 1) sum += __shfl_xor(sum, x);
   __shared__ f32x4v s_acc[kThreads];
   s_acc[threadIdx.x] = acc;
   __syncthreads();
@@ -1035,7 +1035,6 @@ __global__ __launch_bounds__(kThreads) void attention_fold_many_kernel(AttnArgs 
     for (int v = 0; v < 4; ++v) acc[v] *= down;
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
-      // a part that saw no key has nothing but zeros
       const float f = ml[k][0] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml[k][0] - up);
       sum += f * ml[k][1];
 #pragma unroll
