@@ -164,7 +164,7 @@ enum ForkState : int32_t {
   kForkIgnored = 0,    // a repeated or unknown child: nothing of it changes
   kForkSame = 1,       // its own parent: left as it is
   kForkDone = 2,
-  kForkEmptied = 3,    // no such parent, or a page of it is missing: the child is left empty
+  kForkEmptied = 3,    // no such parent, or a page of its length is missing: the child is left empty
   kForkNoPage = 4,     // no page was left for its partial page: left empty
 };
 struct ForkEntry {
@@ -189,11 +189,15 @@ __global__ __launch_bounds__(256) void fork_snapshot_kernel(CacheArgs c, const i
       f.state = kForkEmptied;
       int full = 0;
       if (par >= 0 && par < c.seqs) {
-        f.length = (int32_t)min((int64_t)max(c.lengths[par], 0), c.width << c.page_log2);
+        f.length = max(c.lengths[par], 0);
         full = f.length >> c.page_log2;
         const bool part = (f.length & ((1 << c.page_log2) - 1)) != 0;
-        const int32_t src = part ? c.table[(int64_t)par * c.width + full] : -1;
-        if (!part || page_ok(src, c.pages)) {
+        bool missing = (int64_t)full + part > c.width;
+        const int32_t src = part && !missing ? c.table[(int64_t)par * c.width + full] : -1;
+        missing |= part && !page_ok(src, c.pages);
+        for (int64_t p = tid; !missing && p < full; p += 256)
+          missing = !page_ok(c.table[(int64_t)par * c.width + p], c.pages);
+        if (!__syncthreads_or(missing)) {
           f.state = kForkDone;
           f.src = src;
         }
