@@ -43,7 +43,7 @@ int check_cache(const char* fn, const trellis_kv_cache* c) {
   if (c->heads < 1 || c->heads > 1024) return api_fail(TRELLIS_EINVAL, "%s: heads=%d outside 1..1024", fn, c->heads);
   if (c->layers < 1 || c->layers > 65535)
     return api_fail(TRELLIS_EINVAL, "%s: layers=%d outside 1..65535", fn, c->layers);
-  if (c->pages < 1 || c->pages * c->page_size >= kMaxIndex)
+  if (c->pages < 1 || c->pages >= kMaxIndex || c->pages * c->page_size >= kMaxIndex)
     return api_fail(TRELLIS_EINVAL, "%s: pages=%lld (slots must number 1..2^31-1)", fn, (long long)c->pages);
   return TRELLIS_OK;
 }
