@@ -395,7 +395,8 @@ int trellis_probe_gateup_decode_free(const uint32_t* gcodes, const uint16_t* gsc
  * what it reads there: rows and pages outside the arrays are never touched,
  * keys without storage (a table entry that is no page of the pool, whatever
  * lengths says) are never seen, sequence numbers outside 0..seqs-1 are
- * skipped.
+ * skipped.  They are read more than once: nothing else may write them while
+ * a call runs.
  */
 #define TRELLIS_KV_BF16 0
 #define TRELLIS_KV_F16 1

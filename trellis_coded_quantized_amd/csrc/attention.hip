@@ -567,10 +567,9 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attention_many_k
     at.left = uniform(at.left);
     at.e = __builtin_amdgcn_readfirstlane(at.e);
     at.u = __builtin_amdgcn_readfirstlane(at.u);
-    if (at.left == 0) {
-      if (h == 0 && tid == 0) a.part_note[w] = PartNote{0, 0, 0, 0, 0};
-      return;
-    }
+    // the fold reads a note of every run: none is left as the workspace had it, however the run ends
+    if (h == 0 && tid == 0) a.part_note[w] = PartNote{0, 0, 0, 0, 0};
+    if (at.left == 0) return;
   }
   for (int segment = 0;; ++segment) {
     int rt, first;                                           // the unit, and its tiles before this segment
@@ -616,11 +615,9 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attention_many_k
     const int t1 = __builtin_amdgcn_readfirstlane((int)min((int64_t)list.count, upto));
     if constexpr (!TREE) {
       // this run begins a unit and leaves it to others (its last segment)
-      if (h == 0 && tid == 0 && count >= upto)
-        a.part_note[w] = first == 0 && count > upto
-                             ? PartNote{(int)((count - upto + at.run - 1) / at.run) + 1, e.first, e.n * group,
-                                        rt << 1 | (segment != 0), 0}
-                             : PartNote{0, 0, 0, 0, 0};
+      if (h == 0 && tid == 0 && first == 0 && count > upto)
+        a.part_note[w] = PartNote{(int)((count - upto + at.run - 1) / at.run) + 1, e.first, e.n * group,
+                                  rt << 1 | (segment != 0), 0};
       at.left -= min(upto, (int64_t)count) - first;
     }
 
