@@ -53,6 +53,8 @@ __device__ __forceinline__ Cut find_cut(const AttnArgs& a, int least, const Size
 #pragma unroll
   for (int d = 32; d; d >>= 1) longest = max(longest, __shfl_xor(longest, d));
   longest = __builtin_amdgcn_readfirstlane(longest);
+  // whether one unit is all there is: the only entry's, which is lane 0's
+  const bool single = a.entries == 1 && __builtin_amdgcn_readfirstlane(cut.units) == 1;
   auto slots = [&](int c) {
     int64_t n = (int64_t)((cut.tiles + c - 1) / c) * cut.units;
     for (int b = 64; b < a.entries; b += 64) {
@@ -69,7 +71,7 @@ __device__ __forceinline__ Cut find_cut(const AttnArgs& a, int least, const Size
       cut.chunk = __builtin_amdgcn_readfirstlane(max(longest, 1));
       return cut;
     }
-    if (a.entries == 1 && cut.units == 1) {                  // mean was rounded up: it fits
+    if (single) {                                            // mean was rounded up: it fits
       cut.chunk = __builtin_amdgcn_readfirstlane((int)c);
       return cut;
     }
