@@ -1,5 +1,6 @@
-// What the attention's device headers take from HIP, for one lane at a time on
-// the CPU.  Only code that exchanges nothing between lanes is run this way.
+// What the library's headers take from HIP, for the CPU: device code one lane
+// at a time (only code that exchanges nothing between lanes is run this way),
+// and the host calls that a test stands in for.
 #pragma once
 #include <math.h>
 #include <stddef.h>
@@ -12,6 +13,10 @@ using std::max;
 using std::min;
 typedef int hipError_t;
 typedef void* hipStream_t;
+constexpr hipError_t hipSuccess = 0, hipErrorInvalidDevice = 101;
+constexpr int hipFuncAttributeMaxDynamicSharedMemorySize = 8;
+hipError_t hipGetDevice(int*);
+hipError_t hipFuncSetAttribute(const void*, int, int);
 
 extern unsigned host_lane;
 inline unsigned __lane_id() { return host_lane; }

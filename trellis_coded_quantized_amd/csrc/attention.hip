@@ -1100,16 +1100,9 @@ Parts part_bytes(const AttnArgs& a) {
 template <typename T, int D, int WAVES, bool TREE>
 hipError_t launch_many(AttnArgs& a, hipStream_t stream) {
   constexpr size_t lds = 2 * 2 * (size_t)kManyKeys * D * 2;
-  static uint64_t lds_attr = 0;                // devices whose dynamic LDS limit is raised
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return hipErrorInvalidDevice;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (!(lds_attr & bit)) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&attention_many_kernel<T, D, WAVES, TREE>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (e != hipSuccess) return e;
-    lds_attr |= bit;
-  }
+  static LdsLimit limit;
+  const hipError_t e = limit.raise(reinterpret_cast<const void*>(&attention_many_kernel<T, D, WAVES, TREE>), lds);
+  if (e != hipSuccess) return e;
   a.target = many_target(a);
   a.rounds = rounds_of(a, a.target);
   attention_many_kernel<T, D, WAVES, TREE><<<(unsigned)(a.target * a.heads_kv), Many<WAVES>::kThreads, lds, stream>>>(a);

@@ -43,16 +43,9 @@ __global__ __launch_bounds__(64) void axis0_fold_kernel(const float* __restrict_
 template <int K>
 hipError_t axis0_launch(const uint32_t* codes, const uint16_t* scales, const uint16_t* x, float* partial,
                         const Axis0Geom& g, hipStream_t stream) {
-  static uint64_t lds_attr = 0;                // devices whose dynamic LDS limit is raised
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return hipErrorInvalidDevice;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (!(lds_attr & bit)) {
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&axis0_kernel<K>),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)kLdsBudget);
-    if (e != hipSuccess) return e;
-    lds_attr |= bit;
-  }
+  static LdsLimit limit;
+  const hipError_t e = limit.raise(reinterpret_cast<const void*>(&axis0_kernel<K>), kLdsBudget);
+  if (e != hipSuccess) return e;
   const int units = ((g.ncg + 3) / 4) * g.S;
   const unsigned grid = (unsigned)(4 * kXcds * ((units + kXcds - 1) / kXcds));
   hipLaunchKernelGGL((axis0_kernel<K>), dim3(grid), dim3(kThreads), g.total, stream, codes, scales, x,

@@ -47,16 +47,10 @@ template <int K, bool GU, int NG, bool GROUP = false, bool DECODE = true>
 hipError_t axis1_launch_one(const uint32_t* c0, const uint16_t* s0, const uint32_t* c1,
                             const uint16_t* s1, const uint16_t* x, void* out, int out_f32,
                             float* gf, float* uf, const Axis1Geom& g, int64_t grid, hipStream_t stream) {
-  static uint64_t lds_attr = 0;                // devices whose dynamic LDS limit is raised
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return hipErrorInvalidDevice;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (!(lds_attr & bit)) {
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&axis1_kernel<K, GU, NG, GROUP, DECODE>),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)kAxis1MaxLdsBytes);
-    if (e != hipSuccess) return e;
-    lds_attr |= bit;
-  }
+  static LdsLimit limit;
+  const hipError_t e =
+      limit.raise(reinterpret_cast<const void*>(&axis1_kernel<K, GU, NG, GROUP, DECODE>), kAxis1MaxLdsBytes);
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL((axis1_kernel<K, GU, NG, GROUP, DECODE>), dim3((unsigned)grid), dim3(kThreads), g.total,
                      stream, c0, s0, c1, s1, x, out, out_f32, gf, uf, g);
   return hipGetLastError();

@@ -7,7 +7,27 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace trellis {
+
+// Raises one kernel's limit of dynamic LDS, once for each device.  Calls may
+// come from several threads at a time: two that are both the first raise it
+// twice, which does no harm.
+class LdsLimit {
+  std::atomic<uint64_t> raised_{0};
+
+ public:
+  hipError_t raise(const void* kernel, size_t bytes) {
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return hipErrorInvalidDevice;
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (raised_.load(std::memory_order_acquire) & bit) return hipSuccess;
+    const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == hipSuccess) raised_.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+};
 
 // axis 1 (gate/up when codes1 != nullptr).  The persistent kernel keeps a
 // ring of 16-row code tiles in LDS and x in registers; axis1_supported says
