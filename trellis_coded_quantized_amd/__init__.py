@@ -520,6 +520,13 @@ def _tensor(t, name, dtype, shape, index):
     return t.data_ptr()
 
 
+def _c_int(v, name):
+    """A number that the library takes as a C int; ctypes would drop the bits above."""
+    if not -0x80000000 <= v <= 0x7FFFFFFF:
+        raise ValueError(f"{name}={v} outside 32 bits")
+    return v
+
+
 def _index(t, name):
     """Device number of the tensor that a call runs by."""
     if not isinstance(t, torch.Tensor):
@@ -661,6 +668,7 @@ def tree_attention(q, k_cache, v_cache, table, lengths, q_start, ancestors, max_
     q_start[e+1]-1, at most max_q (<= 64) of them, cached behind `lengths`.
     ancestors int64 [N]: bit m set if the row sees the entry's token m.  scale
     defaults to D ** -0.5.  Returns [N, Hq, D]."""
+    _c_int(max_q, "max_q")
     dev, qp, stride, cache, state, ids, starts, op, n, out = _attention(q, k_cache, v_cache, table, lengths, q_start,
                                                                         seq_ids, out)
     tokens, hq, D = q.shape
@@ -678,6 +686,8 @@ def window_attention(q, k_cache, v_cache, table, lengths, q_start, max_q, window
     """Causal attention of new tokens over the cache: the token at position p
     sees the keys j <= p with p - j < window (0: no limit) or j < sinks.
     Arguments otherwise as tree_attention; max_q has no upper bound."""
+    for name, v in (("max_q", max_q), ("window", window), ("sinks", sinks)):
+        _c_int(v, name)
     dev, qp, stride, cache, state, ids, starts, op, n, out = _attention(q, k_cache, v_cache, table, lengths, q_start,
                                                                         seq_ids, out)
     tokens, hq, D = q.shape
@@ -703,6 +713,7 @@ def kv_state(seqs, width, pages, device="cuda"):
 
 def _state_only(table, lengths, refs, page_size):
     """(cache without pools, state, device number) of the calls that touch no keys or values"""
+    _c_int(page_size, "page_size")
     dev = _index(refs, "refs")
     if refs.dim() != 1:
         raise ValueError(f"refs: expected [pages], got shape {tuple(refs.shape)}")
