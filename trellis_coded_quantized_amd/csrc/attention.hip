@@ -356,9 +356,9 @@ struct Many {
 };
 // Waves of a workgroup, by the rows that an entry can have.  Where 128 rows do,
 // two workgroups of four waves have twice the loads under way on a compute
-// unit: 64 trees of 16 tokens over 4096 keys, 32 / 8 heads of 128, 240 us
-// against 300 (heads of 64: 148 against 219).  A single entry loses to
-// the doubled parts (32 tokens over 30000 keys: 44 us against 41).
+// unit: 64 trees of 16 tokens over 4096 keys, 32 / 8 heads of 128, 212 us
+// against 247 (heads of 64: 140 against 183).  A single entry loses to
+// the doubled parts (32 tokens over 30000 keys: 43 us against 40).
 constexpr int64_t kHalfRows = 128;
 inline int many_waves(const AttnArgs& a) {
   return a.head_dim == 256 || (int64_t)a.max_q * (a.heads_q / a.heads_kv) <= kHalfRows ? 4 : 8;
