@@ -536,6 +536,92 @@ int trellis_cache_accept(const trellis_kv_cache* cache, const trellis_kv_state* 
 int trellis_cache_free(const trellis_kv_cache* cache, const trellis_kv_state* state, const int32_t* seq_ids, int n,
                        void* stream);
 
+/*
+ * ---- the cache held in 8 bits ---------------------------------------------
+ *
+ * trellis_kv8_cache -- a paged cache of e4m3 numbers (4 significant bits,
+ * largest 448, no infinities) in half the memory of trellis_kv_cache.  16
+ * consecutive tokens of a page and head are a block; a block's keys have one
+ * power-of-two scale and its values another, bytes b that stand for
+ * 2^(b - 127) (E8M0).  An element is code * scale.  Layouts, of bytes:
+ *   k [layers, pages, heads, head_dim/16, P, 16]
+ *   v [layers, pages, heads, P/16, head_dim, 16]
+ *   k_scale, v_scale [layers, pages, heads, P/16]
+ * i.e. dimension d of token t of a page is byte
+ *   k: (((page * heads + h) * head_dim/16 + d/16) * P + t) * 16 + d%16
+ *   v: (((page * heads + h) * P/16 + t/16) * head_dim + d) * 16 + t%16
+ * under scale (page * heads + h) * P/16 + t/16.  dtype (TRELLIS_KV_BF16 or
+ * TRELLIS_KV_F16) is the 16-bit type of the other tensors of a call.  Sizes
+ * as for trellis_kv_cache; k and v are 16-byte aligned.  Tables, lengths and
+ * reference counts are the same trellis_kv_state; trellis_cache_reserve and
+ * trellis_cache_free, which touch no keys or values, serve both caches.
+ * The caller starts with scales of 0 (2^-127) or anything else.
+ *
+ * trellis_qk_norm_rope_kv8 -- trellis_qk_norm_rope into this cache.  New
+ * tokens are rounded once, from f32, to the nearest code (ties to even) under
+ * their block's scale:
+ *   need(block) = the smallest b of 1..254 with 448 * 2^(b - 127) >= the
+ *                 largest finite magnitude of the block's new elements
+ *   b' = need            where a new token takes the block's first slot: the
+ *                        block begins anew, what its other slots held is void
+ *   b' = max(b, need)    elsewhere; where that is more than b, the block's
+ *                        other tokens are rounded again under b' (exact but
+ *                        for codes that fall below e4m3's normal numbers)
+ * Infinities and NaN are stored as NaN and do not count for the scale.
+ * Magnitudes above the largest number with 4 significant bits of the 16-bit
+ * type (bf16 1.875 * 2^127, fp16 61440) are stored as that number.
+ * Tokens whose slots lie in one block stand next to each other in the list
+ * (trellis_cache_reserve's order is like that), in any order; what a block
+ * holds is undefined, but nothing else, where they do not, and where two
+ * tokens share a slot.
+ *
+ * trellis_window_attention_kv8, trellis_tree_attention_kv8 -- the attention
+ * calls over this cache, with the same arguments, rules and workspace.  Codes
+ * enter the products as code * scale in the 16-bit type: exact in bf16 and in
+ * fp16's normal numbers, rounded once below those.
+ *
+ * trellis_cache_fork_kv8 -- trellis_cache_fork; scales are copied with the
+ * page.
+ *
+ * trellis_cache_accept_kv8 -- trellis_cache_accept.  A block that rows move
+ * into takes the largest of its own scale and those of the rows' blocks; its
+ * rows are rounded again under that.
+ */
+typedef struct trellis_kv8_cache {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  int64_t pages;
+  int layers, heads, head_dim, page_size, dtype;
+} trellis_kv8_cache;
+
+int trellis_qk_norm_rope_kv8(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                             const uint16_t* v, int64_t v_stride, const uint16_t* q_weight, const uint16_t* k_weight,
+                             const int32_t* positions, const float* inv_freq, int rotary_dim, int interleaved,
+                             float eps, const int32_t* slots, uint16_t* out, const trellis_kv8_cache* cache,
+                             int64_t tokens, int heads_q, void* stream);
+size_t trellis_tree_attention_kv8_workspace_bytes(const trellis_kv8_cache* cache, const trellis_kv_state* state, int n,
+                                                  int64_t tokens, int heads_q, int max_q);
+int trellis_tree_attention_kv8(const uint16_t* q, int64_t q_stride, const trellis_kv8_cache* cache,
+                               const trellis_kv_state* state, const int32_t* seq_ids, int n, const int32_t* q_start,
+                               const int64_t* ancestors, int64_t tokens, int heads_q, int max_q, float scale,
+                               uint16_t* out, void* workspace, size_t workspace_bytes, void* stream);
+size_t trellis_window_attention_kv8_workspace_bytes(const trellis_kv8_cache* cache, const trellis_kv_state* state,
+                                                    int n, int64_t tokens, int heads_q, int max_q, int window,
+                                                    int sinks);
+int trellis_window_attention_kv8(const uint16_t* q, int64_t q_stride, const trellis_kv8_cache* cache,
+                                 const trellis_kv_state* state, const int32_t* seq_ids, int n, const int32_t* q_start,
+                                 int64_t tokens, int heads_q, int max_q, int window, int sinks, float scale,
+                                 uint16_t* out, void* workspace, size_t workspace_bytes, void* stream);
+size_t trellis_cache_fork_kv8_workspace_bytes(const trellis_kv8_cache* cache, const trellis_kv_state* state, int n);
+int trellis_cache_fork_kv8(const trellis_kv8_cache* cache, const trellis_kv_state* state, const int32_t* parents,
+                           const int32_t* children, int n, int32_t* granted, void* workspace, size_t workspace_bytes,
+                           void* stream);
+int trellis_cache_accept_kv8(const trellis_kv8_cache* cache, const trellis_kv_state* state, const int32_t* seq_ids,
+                             int n, const int32_t* path, int max_path, const int32_t* counts, int32_t* new_lengths,
+                             void* stream);
+
 /* Description of the last non-OK status on this thread ("" if none). */
 const char* trellis_last_error(void);
 

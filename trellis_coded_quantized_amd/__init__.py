@@ -18,6 +18,11 @@ Attention between the projections (one paged key/value cache):
   v_cache  the same type    [(layers,) pages, kv_heads, P/8, D, 8]
   table    int32 [seqs, width] page numbers, -1: none
   lengths  int32 [seqs] cached tokens;  refs  int32 [pages] holders of a page
+
+The same over a cache held in 8 bits (calls ending in _kv8):
+  k_cache  float8_e4m3fn [(layers,) pages, kv_heads, D/16, P, 16]
+  v_cache  float8_e4m3fn [(layers,) pages, kv_heads, P/16, D, 16]
+  k_scale, v_scale  float8_e8m0fnu [(layers,) pages, kv_heads, P/16]
 """
 import ctypes
 import os
@@ -53,6 +58,10 @@ EXPORTS = (
     "trellis_window_attention_workspace_bytes", "trellis_window_attention",
     "trellis_cache_reserve_workspace_bytes", "trellis_cache_reserve",
     "trellis_cache_fork_workspace_bytes", "trellis_cache_fork", "trellis_cache_accept", "trellis_cache_free",
+    "trellis_qk_norm_rope_kv8",
+    "trellis_tree_attention_kv8_workspace_bytes", "trellis_tree_attention_kv8",
+    "trellis_window_attention_kv8_workspace_bytes", "trellis_window_attention_kv8",
+    "trellis_cache_fork_kv8_workspace_bytes", "trellis_cache_fork_kv8", "trellis_cache_accept_kv8",
     "trellis_decode_states", "trellis_last_error", "trellis_version",
 )
 
@@ -66,6 +75,14 @@ class TrellisError(RuntimeError):
 class KvCache(ctypes.Structure):
     """trellis_kv_cache of include/trellis.h"""
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", ctypes.c_int64), ("layers", ctypes.c_int),
+                ("heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("dtype", ctypes.c_int)]
+
+
+class Kv8Cache(ctypes.Structure):
+    """trellis_kv8_cache of include/trellis.h"""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("layers", ctypes.c_int),
                 ("heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("page_size", ctypes.c_int),
                 ("dtype", ctypes.c_int)]
 
@@ -138,6 +155,18 @@ def load_library():
         "trellis_cache_fork": (_int, [_vp, _vp, _vp, _vp, _int, _vp, _vp, _sz, _vp]),
         "trellis_cache_accept": (_int, [_vp, _vp, _vp, _int, _vp, _int, _vp, _vp, _vp]),
         "trellis_cache_free": (_int, [_vp, _vp, _vp, _int, _vp]),
+        **{"trellis_" + name + "_kv8" + more: sig_of for name, more, sig_of in (
+            ("tree_attention", "_workspace_bytes", (_sz, [_vp, _vp, _int, _i64, _int, _int])),
+            ("tree_attention", "", (_int, [_vp, _i64, _vp, _vp, _vp, _int, _vp, _vp, _i64, _int, _int,
+                                           ctypes.c_float, _vp, _vp, _sz, _vp])),
+            ("window_attention", "_workspace_bytes", (_sz, [_vp, _vp, _int, _i64, _int, _int, _int, _int])),
+            ("window_attention", "", (_int, [_vp, _i64, _vp, _vp, _vp, _int, _vp, _i64, _int, _int, _int, _int,
+                                             ctypes.c_float, _vp, _vp, _sz, _vp])),
+            ("qk_norm_rope", "", (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _int, _int,
+                                         ctypes.c_float, _vp, _vp, _vp, _i64, _int, _vp])),
+            ("cache_fork", "_workspace_bytes", (_sz, [_vp, _vp, _int])),
+            ("cache_fork", "", (_int, [_vp, _vp, _vp, _vp, _int, _vp, _vp, _sz, _vp])),
+            ("cache_accept", "", (_int, [_vp, _vp, _vp, _int, _vp, _int, _vp, _vp, _vp])))},
         "trellis_last_error": (ctypes.c_char_p, []),
         "trellis_version": (ctypes.c_char_p, []),
     }
@@ -593,6 +622,36 @@ def _kv_cache(k_cache, v_cache, layered):
                    _KV[dtype]), index
 
 
+_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def _type_of(q):
+    """The 16-bit type of a call over an 8-bit cache: that of its queries."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    if q.dtype not in _KV:
+        raise TypeError(f"q: dtype {q.dtype} not in {tuple(_KV)}")
+    return q.dtype
+
+
+def _kv8_cache(k_cache, v_cache, k_scale, v_scale, dtype, layered):
+    """(Kv8Cache of the pools and scales after checking that they are one cache, device number)."""
+    index = _index(k_cache, "k_cache")
+    shape = k_cache.shape
+    n = len(shape)
+    if n != 5 and not (layered and n == 6) or shape[-1] != 16:
+        raise ValueError(f"k_cache: expected {'[layers, ' if layered else 'one layer ['}pages, heads, D/16, P, 16], got "
+                         f"shape {tuple(shape)}")
+    lead = tuple(shape[:-3])                                   # (layers,) pages, heads
+    blocks, page_size = shape[-3], shape[-2]
+    k = _tensor(k_cache, "k_cache", _E4M3, shape, index)
+    v = _tensor(v_cache, "v_cache", _E4M3, lead + (page_size // 16, blocks * 16, 16), index)
+    ks = _tensor(k_scale, "k_scale", _E8M0, lead + (page_size // 16,), index)
+    vs = _tensor(v_scale, "v_scale", _E8M0, lead + (page_size // 16,), index)
+    return Kv8Cache(k, v, ks, vs, lead[-2], lead[0] if n == 6 else 1, lead[-1], blocks * 16, page_size,
+                    _KV[dtype]), index
+
+
 def _kv_state(table, lengths, refs, pages, index):
     t = _tensor(table, "table", torch.int32, (None, None), index)
     seqs, width = table.shape
@@ -618,14 +677,9 @@ def _head_rows(t, name, heads, head_dim, dtype, index):
     return t.data_ptr(), row if n > 1 else h * head_dim
 
 
-def qk_norm_rope(q, k, v, q_weight, k_weight, positions, inv_freq, slots, k_cache, v_cache, eps=1e-6,
-                 interleaved=False, out=None):
-    """RMS norm of every head of q [N, Hq, D] and k [N, Hkv, D], rotation of the
-    first 2 * len(inv_freq) dimensions by positions * inv_freq, and the append
-    of k and v to the cache at `slots` (int32 [N], -1: not cached).  q, k and v
-    may be views of one projection output.  Returns the queries [N, Hq, D]."""
-    cache, dev = _kv_cache(k_cache, v_cache, False)
-    D, dt, i32 = cache.head_dim, k_cache.dtype, torch.int32
+def _append(fn, cache, dev, dt, q, k, v, q_weight, k_weight, positions, inv_freq, slots, eps, interleaved, out):
+    """What the two appends share; dt is the 16-bit type of the call."""
+    D, i32 = cache.head_dim, torch.int32
     qp, qs = _head_rows(q, "q", None, D, dt, dev)
     kp, ks = _head_rows(k, "k", cache.heads, D, dt, dev)
     vp, vs = _head_rows(v, "v", cache.heads, D, dt, dev)
@@ -637,17 +691,38 @@ def qk_norm_rope(q, k, v, q_weight, k_weight, positions, inv_freq, slots, k_cach
     inv = _tensor(inv_freq, "inv_freq", torch.float32, (None,), dev)
     pos = _tensor(positions, "positions", i32, (N,), dev)
     at = _tensor(slots, "slots", i32, (N,), dev)
-    out, op = _result(out, "out", (N, hq, D), dt, k_cache.device, dev)
-    _call(load_library().trellis_qk_norm_rope, dev, qp, qs, kp, ks, vp, vs, wq, wk, pos, inv, 2 * inv_freq.shape[0],
-          interleaved, eps, at, op, _byref(cache), N, hq)
+    out, op = _result(out, "out", (N, hq, D), dt, q.device, dev)
+    _call(fn, dev, qp, qs, kp, ks, vp, vs, wq, wk, pos, inv, 2 * inv_freq.shape[0], interleaved, eps, at, op,
+          _byref(cache), N, hq)
     return out
 
 
-def _attention(q, k_cache, v_cache, table, lengths, q_start, seq_ids, out):
-    """What the two attention calls share: (device number, q's address and stride, cache, state, addresses of seq_ids,
-    q_start and out, entries, out)."""
+def qk_norm_rope(q, k, v, q_weight, k_weight, positions, inv_freq, slots, k_cache, v_cache, eps=1e-6,
+                 interleaved=False, out=None):
+    """RMS norm of every head of q [N, Hq, D] and k [N, Hkv, D], rotation of the
+    first 2 * len(inv_freq) dimensions by positions * inv_freq, and the append
+    of k and v to the cache at `slots` (int32 [N], -1: not cached).  q, k and v
+    may be views of one projection output.  Returns the queries [N, Hq, D]."""
     cache, dev = _kv_cache(k_cache, v_cache, False)
-    dt = k_cache.dtype
+    return _append(load_library().trellis_qk_norm_rope, cache, dev, k_cache.dtype, q, k, v, q_weight, k_weight,
+                   positions, inv_freq, slots, eps, interleaved, out)
+
+
+def qk_norm_rope_kv8(q, k, v, q_weight, k_weight, positions, inv_freq, slots, k_cache, v_cache, k_scale, v_scale,
+                     eps=1e-6, interleaved=False, out=None):
+    """qk_norm_rope into a cache held in 8 bits.  Tokens whose slots lie in one
+    block of 16 stand next to each other in the list, as cache_reserve gives
+    them.  A block's scale grows with its tokens, and begins anew with its
+    first slot."""
+    dt = _type_of(q)
+    cache, dev = _kv8_cache(k_cache, v_cache, k_scale, v_scale, dt, False)
+    return _append(load_library().trellis_qk_norm_rope_kv8, cache, dev, dt, q, k, v, q_weight, k_weight, positions,
+                   inv_freq, slots, eps, interleaved, out)
+
+
+def _attention(q, cache, dev, dt, table, lengths, q_start, seq_ids, out):
+    """What the attention calls share: (q's address and stride, state, addresses of seq_ids, q_start and out,
+    entries, out)."""
     qp, stride = _head_rows(q, "q", None, cache.head_dim, dt, dev)
     state = _kv_state(table, lengths, None, cache.pages, dev)
     starts = _tensor(q_start, "q_start", torch.int32, (None,), dev)
@@ -657,8 +732,35 @@ def _attention(q, k_cache, v_cache, table, lengths, q_start, seq_ids, out):
         ids = _tensor(seq_ids, "seq_ids", torch.int32, (n,), dev)
     elif n > state.seqs:
         raise ValueError(f"q_start has {n} entries, the table {state.seqs} sequences")
-    out, op = _result(out, "out", tuple(q.shape), dt, k_cache.device, dev)
-    return dev, qp, stride, cache, state, ids, starts, op, n, out
+    out, op = _result(out, "out", tuple(q.shape), dt, q.device, dev)
+    return qp, stride, state, ids, starts, op, n, out
+
+
+def _tree(fn, sizes, cache, dev, dt, q, table, lengths, q_start, ancestors, max_q, scale, seq_ids, out, workspace):
+    qp, stride, state, ids, starts, op, n, out = _attention(q, cache, dev, dt, table, lengths, q_start, seq_ids, out)
+    tokens, hq, D = q.shape
+    anc = _tensor(ancestors, "ancestors", torch.int64, (tokens,), dev)
+    c, s = _byref(cache), _byref(state)
+    _keep, ws, wsb = _scratch(sizes(c, s, n, tokens, hq, max_q), q.device, workspace)
+    _call(fn, dev, qp, stride, c, s, ids, n, starts, anc, tokens, hq, max_q, D ** -0.5 if scale is None else scale, op,
+          ws, wsb)
+    return out
+
+
+def _window_numbers(max_q, window, sinks):
+    for name, v in (("max_q", max_q), ("window", window), ("sinks", sinks)):
+        _c_int(v, name)
+
+
+def _window(fn, sizes, cache, dev, dt, q, table, lengths, q_start, max_q, window, sinks, scale, seq_ids, out,
+            workspace):
+    qp, stride, state, ids, starts, op, n, out = _attention(q, cache, dev, dt, table, lengths, q_start, seq_ids, out)
+    tokens, hq, D = q.shape
+    c, s = _byref(cache), _byref(state)
+    _keep, ws, wsb = _scratch(sizes(c, s, n, tokens, hq, max_q, window, sinks), q.device, workspace)
+    _call(fn, dev, qp, stride, c, s, ids, n, starts, tokens, hq, max_q, window, sinks,
+          D ** -0.5 if scale is None else scale, op, ws, wsb)
+    return out
 
 
 def tree_attention(q, k_cache, v_cache, table, lengths, q_start, ancestors, max_q, scale=None, seq_ids=None, out=None,
@@ -669,16 +771,10 @@ def tree_attention(q, k_cache, v_cache, table, lengths, q_start, ancestors, max_
     ancestors int64 [N]: bit m set if the row sees the entry's token m.  scale
     defaults to D ** -0.5.  Returns [N, Hq, D]."""
     _c_int(max_q, "max_q")
-    dev, qp, stride, cache, state, ids, starts, op, n, out = _attention(q, k_cache, v_cache, table, lengths, q_start,
-                                                                        seq_ids, out)
-    tokens, hq, D = q.shape
-    anc = _tensor(ancestors, "ancestors", torch.int64, (tokens,), dev)
-    lib, c, s = load_library(), _byref(cache), _byref(state)
-    _keep, ws, wsb = _scratch(lib.trellis_tree_attention_workspace_bytes(c, s, n, tokens, hq, max_q), q.device,
-                              workspace)
-    _call(lib.trellis_tree_attention, dev, qp, stride, c, s, ids, n, starts, anc, tokens, hq, max_q,
-          D ** -0.5 if scale is None else scale, op, ws, wsb)
-    return out
+    cache, dev = _kv_cache(k_cache, v_cache, False)
+    lib = load_library()
+    return _tree(lib.trellis_tree_attention, lib.trellis_tree_attention_workspace_bytes, cache, dev, k_cache.dtype, q,
+                 table, lengths, q_start, ancestors, max_q, scale, seq_ids, out, workspace)
 
 
 def window_attention(q, k_cache, v_cache, table, lengths, q_start, max_q, window=0, sinks=0, scale=None, seq_ids=None,
@@ -686,23 +782,48 @@ def window_attention(q, k_cache, v_cache, table, lengths, q_start, max_q, window
     """Causal attention of new tokens over the cache: the token at position p
     sees the keys j <= p with p - j < window (0: no limit) or j < sinks.
     Arguments otherwise as tree_attention; max_q has no upper bound."""
-    for name, v in (("max_q", max_q), ("window", window), ("sinks", sinks)):
-        _c_int(v, name)
-    dev, qp, stride, cache, state, ids, starts, op, n, out = _attention(q, k_cache, v_cache, table, lengths, q_start,
-                                                                        seq_ids, out)
-    tokens, hq, D = q.shape
-    lib, c, s = load_library(), _byref(cache), _byref(state)
-    _keep, ws, wsb = _scratch(lib.trellis_window_attention_workspace_bytes(c, s, n, tokens, hq, max_q, window, sinks),
-                              q.device, workspace)
-    _call(lib.trellis_window_attention, dev, qp, stride, c, s, ids, n, starts, tokens, hq, max_q, window, sinks,
-          D ** -0.5 if scale is None else scale, op, ws, wsb)
-    return out
+    _window_numbers(max_q, window, sinks)
+    cache, dev = _kv_cache(k_cache, v_cache, False)
+    lib = load_library()
+    return _window(lib.trellis_window_attention, lib.trellis_window_attention_workspace_bytes, cache, dev,
+                   k_cache.dtype, q, table, lengths, q_start, max_q, window, sinks, scale, seq_ids, out, workspace)
+
+
+def tree_attention_kv8(q, k_cache, v_cache, k_scale, v_scale, table, lengths, q_start, ancestors, max_q, scale=None,
+                       seq_ids=None, out=None, workspace=None):
+    """tree_attention over a cache held in 8 bits; q and the result are bf16 or fp16."""
+    _c_int(max_q, "max_q")
+    dt = _type_of(q)
+    cache, dev = _kv8_cache(k_cache, v_cache, k_scale, v_scale, dt, False)
+    lib = load_library()
+    return _tree(lib.trellis_tree_attention_kv8, lib.trellis_tree_attention_kv8_workspace_bytes, cache, dev, dt, q,
+                 table, lengths, q_start, ancestors, max_q, scale, seq_ids, out, workspace)
+
+
+def window_attention_kv8(q, k_cache, v_cache, k_scale, v_scale, table, lengths, q_start, max_q, window=0, sinks=0,
+                         scale=None, seq_ids=None, out=None, workspace=None):
+    """window_attention over a cache held in 8 bits; q and the result are bf16 or fp16."""
+    _window_numbers(max_q, window, sinks)
+    dt = _type_of(q)
+    cache, dev = _kv8_cache(k_cache, v_cache, k_scale, v_scale, dt, False)
+    lib = load_library()
+    return _window(lib.trellis_window_attention_kv8, lib.trellis_window_attention_kv8_workspace_bytes, cache, dev, dt,
+                   q, table, lengths, q_start, max_q, window, sinks, scale, seq_ids, out, workspace)
 
 
 def kv_cache(layers, pages, heads, head_dim, page_size, dtype=torch.bfloat16, device="cuda"):
     """Empty pools (k_cache, v_cache) of `layers` layers; k_cache[i], v_cache[i] are one layer."""
     k = torch.zeros((layers, pages, heads, head_dim // 8, page_size, 8), dtype=dtype, device=device)
     return k, torch.zeros((layers, pages, heads, page_size // 8, head_dim, 8), dtype=dtype, device=device)
+
+
+def kv8_cache(layers, pages, heads, head_dim, page_size, device="cuda"):
+    """Empty pools and scales (k_cache, v_cache, k_scale, v_scale) of `layers` layers in 8 bits; [i] is one layer."""
+    def zeros(dtype, *shape):
+        return torch.zeros((layers, pages, heads) + shape, dtype=torch.uint8, device=device).view(dtype)
+
+    return (zeros(_E4M3, head_dim // 16, page_size, 16), zeros(_E4M3, page_size // 16, head_dim, 16),
+            zeros(_E8M0, page_size // 16), zeros(_E8M0, page_size // 16))
 
 
 def kv_state(seqs, width, pages, device="cuda"):
@@ -739,26 +860,37 @@ def cache_reserve(table, lengths, refs, page_size, seq_ids, q_start, tokens, slo
     return slots, granted
 
 
-def cache_fork(k_cache, v_cache, table, lengths, refs, parents, children, granted=None, workspace=None):
-    """children[b] becomes a copy of parents[b]: full pages shared, the last
-    partial page copied in every layer.  Returns granted int32 [n]."""
-    cache, dev = _kv_cache(k_cache, v_cache, True)
+def _fork(fn, sizes, cache, dev, device, table, lengths, refs, parents, children, granted, workspace):
     state = _kv_state(table, lengths, refs, cache.pages, dev)
     par = _tensor(parents, "parents", torch.int32, (None,), dev)
     n = parents.shape[0]
     kid = _tensor(children, "children", torch.int32, (n,), dev)
-    granted, gp = _result(granted, "granted", (n,), torch.int32, k_cache.device, dev)
-    lib, c, s = load_library(), _byref(cache), _byref(state)
-    _keep, ws, wsb = _scratch(lib.trellis_cache_fork_workspace_bytes(c, s, n), k_cache.device, workspace)
-    _call(lib.trellis_cache_fork, dev, c, s, par, kid, n, gp, ws, wsb)
+    granted, gp = _result(granted, "granted", (n,), torch.int32, device, dev)
+    c, s = _byref(cache), _byref(state)
+    _keep, ws, wsb = _scratch(sizes(c, s, n), device, workspace)
+    _call(fn, dev, c, s, par, kid, n, gp, ws, wsb)
     return granted
 
 
-def cache_accept(k_cache, v_cache, table, lengths, seq_ids, path, counts, new_lengths=None):
-    """Drafted rows path[b][: counts[b]] of sequence seq_ids[b] move up behind its
-    cached tokens in every layer; lengths grows by counts (in place, or into
-    new_lengths).  Returns the new lengths."""
+def cache_fork(k_cache, v_cache, table, lengths, refs, parents, children, granted=None, workspace=None):
+    """children[b] becomes a copy of parents[b]: full pages shared, the last
+    partial page copied in every layer.  Returns granted int32 [n]."""
     cache, dev = _kv_cache(k_cache, v_cache, True)
+    lib = load_library()
+    return _fork(lib.trellis_cache_fork, lib.trellis_cache_fork_workspace_bytes, cache, dev, k_cache.device, table,
+                 lengths, refs, parents, children, granted, workspace)
+
+
+def cache_fork_kv8(k_cache, v_cache, k_scale, v_scale, table, lengths, refs, parents, children, granted=None,
+                   workspace=None):
+    """cache_fork of a cache held in 8 bits."""
+    cache, dev = _kv8_cache(k_cache, v_cache, k_scale, v_scale, torch.bfloat16, True)
+    lib = load_library()
+    return _fork(lib.trellis_cache_fork_kv8, lib.trellis_cache_fork_kv8_workspace_bytes, cache, dev, k_cache.device,
+                 table, lengths, refs, parents, children, granted, workspace)
+
+
+def _accept(fn, cache, dev, table, lengths, seq_ids, path, counts, new_lengths):
     state, i32 = _kv_state(table, lengths, None, cache.pages, dev), torch.int32
     ids = _tensor(seq_ids, "seq_ids", i32, (None,), dev)
     n = seq_ids.shape[0]
@@ -767,8 +899,24 @@ def cache_accept(k_cache, v_cache, table, lengths, seq_ids, path, counts, new_le
     if new_lengths is None:
         new_lengths = lengths
     to = _tensor(new_lengths, "new_lengths", i32, (state.seqs,), dev)
-    _call(load_library().trellis_cache_accept, dev, _byref(cache), _byref(state), ids, n, pp, path.shape[1], cp, to)
+    _call(fn, dev, _byref(cache), _byref(state), ids, n, pp, path.shape[1], cp, to)
     return new_lengths
+
+
+def cache_accept(k_cache, v_cache, table, lengths, seq_ids, path, counts, new_lengths=None):
+    """Drafted rows path[b][: counts[b]] of sequence seq_ids[b] move up behind its
+    cached tokens in every layer; lengths grows by counts (in place, or into
+    new_lengths).  Returns the new lengths."""
+    cache, dev = _kv_cache(k_cache, v_cache, True)
+    return _accept(load_library().trellis_cache_accept, cache, dev, table, lengths, seq_ids, path, counts, new_lengths)
+
+
+def cache_accept_kv8(k_cache, v_cache, k_scale, v_scale, table, lengths, seq_ids, path, counts, new_lengths=None):
+    """cache_accept in a cache held in 8 bits.  Blocks that rows move into take the
+    largest scale of what they hold; their rows are rounded again under it."""
+    cache, dev = _kv8_cache(k_cache, v_cache, k_scale, v_scale, torch.bfloat16, True)
+    return _accept(load_library().trellis_cache_accept_kv8, cache, dev, table, lengths, seq_ids, path, counts,
+                   new_lengths)
 
 
 def cache_free(table, lengths, refs, seq_ids):

@@ -8,7 +8,7 @@
 // every outcome is determined by the arguments, and a step that changes the
 // cache can be captured into a graph without the host knowing any length.
 #include "internal.hpp"
-#include "kv_common.hpp"
+#include "kv8_common.hpp"
 
 namespace trellis {
 namespace {
@@ -234,9 +234,10 @@ __global__ __launch_bounds__(kPlan) void fork_plan_kernel(CacheArgs c, int n, Fo
 }
 
 // Children's rows and lengths; the copy of the partial page in every layer
-// (blockIdx.y: layer).
+// (blockIdx.y: layer), of 8-bit caches (SCALED) with its scales.
+template <bool SCALED>
 __global__ __launch_bounds__(256) void fork_write_kernel(CacheArgs c, const int32_t* children, const ForkEntry* entries,
-                                                         const int32_t* rows, int32_t* granted) {
+                                                         const int32_t* rows, int32_t* granted, Scales scales) {
   const int b = blockIdx.x, tid = threadIdx.x;
   const ForkEntry f = entries[b];
   if (blockIdx.y == 0) {
@@ -265,7 +266,7 @@ __global__ __launch_bounds__(256) void fork_write_kernel(CacheArgs c, const int3
     }
   }
   if (f.state != kForkDone || f.page < 0) return;
-  const int64_t granules = ((int64_t)c.heads * c.head_dim << c.page_log2) / 8;      // one page of one layer
+  const int64_t granules = ((int64_t)c.heads * c.head_dim << c.page_log2) / (SCALED ? 16 : 8);   // one page of one layer
   const int64_t layer = (int64_t)blockIdx.y * c.pages;
   const u32x4v* ks = reinterpret_cast<const u32x4v*>(c.k) + (layer + f.src) * granules;
   const u32x4v* vs = reinterpret_cast<const u32x4v*>(c.v) + (layer + f.src) * granules;
@@ -275,6 +276,13 @@ __global__ __launch_bounds__(256) void fork_write_kernel(CacheArgs c, const int3
     const u32x4v x = ks[g], y = vs[g];
     kd[g] = x;
     vd[g] = y;
+  }
+  if constexpr (SCALED) {
+    const int64_t blocks = (int64_t)c.heads << (c.page_log2 - 4), src = (layer + f.src) * blocks, dst = (layer + f.page) * blocks;
+    for (int64_t x = tid; x < blocks; x += 256) {
+      scales.k[dst + x] = scales.k[src + x];
+      scales.v[dst + x] = scales.v[src + x];
+    }
   }
 }
 
@@ -341,6 +349,105 @@ __global__ __launch_bounds__(256) void accept_kernel(CacheArgs c, const int32_t*
   }
 }
 
+// The same over 8-bit blocks.  All rows that move, and their scales, are in LDS
+// before any block changes; then a thread owns a granule of the blocks that
+// rows move into: it sets the rows that arrive and rounds the others again
+// where the block's scale grew.  The scales are written at the end, from what
+// all threads read at the start.
+constexpr int kAcceptBlocks = kCacheMaxPath / 16 + 1;
+__global__ __launch_bounds__(256) void accept_kv8_kernel(CacheArgs c, Scales scales, const int32_t* seq_ids, int n,
+                                                         const int32_t* path, int max_path, const int32_t* counts,
+                                                         int32_t* new_lengths) {
+  if ((int)blockIdx.x == n) {
+    if (blockIdx.y == 0 && blockIdx.z == 0) accept_lengths(c, seq_ids, n, max_path, counts, new_lengths);
+    return;
+  }
+  extern __shared__ __align__(16) u32x4v lds[];              // keys [row][D / 16], values [row][D / 16]
+  __shared__ int s_moves[kCacheMaxPath];
+  __shared__ uint32_t s_from[2][kCacheMaxPath], s_old[2][kAcceptBlocks], s_new[2][kAcceptBlocks];
+  const int b = blockIdx.x, layer = blockIdx.y, h = blockIdx.z, tid = threadIdx.x;
+  const int count = min(max(counts[b], 0), max_path);
+  if (count == 0 || !first_of_its_name(seq_ids, b, c.seqs)) return;
+  const int64_t row = seq_ids[b], len = max(c.lengths[row], 0), P = 1 << c.page_log2;
+  const int D = c.head_dim, gran = D / 16;
+  const uint8_t *k8 = reinterpret_cast<const uint8_t*>(c.k), *v8 = reinterpret_cast<const uint8_t*>(c.v);
+  // the head's page that holds a token, counted over the pool, or -1
+  auto page_of = [&](int64_t at) -> int64_t {
+    const int64_t p = at >> c.page_log2;
+    if (at < 0 || p >= c.width) return -1;
+    const int32_t page = c.table[row * c.width + p];
+    if (!page_ok(page, c.pages)) return -1;
+    return ((int64_t)layer * c.pages + page) * c.heads + h;
+  };
+  auto scale_at = [&](int64_t page, int64_t at) { return (page << (c.page_log2 - 4)) + ((at & (P - 1)) >> 4); };
+  const int64_t head_bytes = (int64_t)D << c.page_log2;
+  const int64_t from_block = len >> 4;                       // the first that a row can move into
+  const int blocks = (int)(((len + count - 1) >> 4) - from_block) + 1;
+  for (int j = tid; j < count; j += 256) {
+    const int from = path[(int64_t)b * max_path + j];
+    const int64_t src = page_of(len + from);
+    const bool moves = from != j && from >= 0 && src >= 0 && page_of(len + j) >= 0;
+    s_moves[j] = moves;
+    s_from[0][j] = moves ? scales.k[scale_at(src, len + from)] : 0;
+    s_from[1][j] = moves ? scales.v[scale_at(src, len + from)] : 0;
+  }
+  for (int x = tid; x < 2 * blocks; x += 256) {
+    const int64_t at = (from_block + (x >> 1)) << 4, page = page_of(at);
+    s_old[x & 1][x >> 1] = s_new[x & 1][x >> 1] = page < 0 ? 0u : (x & 1 ? scales.v : scales.k)[scale_at(page, at)];
+  }
+  __syncthreads();
+  for (int j = tid; j < 2 * count; j += 256)
+    if (s_moves[j >> 1])
+      atomicMax(&s_new[j & 1][((len + (j >> 1)) >> 4) - from_block], s_from[j & 1][j >> 1]);
+  u32x4v* lk = lds;
+  uint8_t* lv = reinterpret_cast<uint8_t*>(lds + max_path * gran);
+  for (int x = tid; x < count * gran; x += 256) {
+    const int j = x / gran, g = x % gran;
+    if (!s_moves[j]) continue;
+    const int64_t at = len + path[(int64_t)b * max_path + j], in = at & (P - 1), src = page_of(at) * head_bytes;
+    lk[x] = *reinterpret_cast<const u32x4v*>(k8 + src + (g * P + in) * 16);
+    const uint8_t* vs = v8 + src + ((in >> 4) * D + g * 16) * 16 + (in & 15);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) lv[x * 16 + e] = vs[e * 16];
+  }
+  __syncthreads();
+  // keys: granules [block][D / 16][16 rows]; values: [block][D]
+  for (int x = tid; x < 2 * blocks * D; x += 256) {
+    const bool is_v = x >= blocks * D;
+    const int y = is_v ? x - blocks * D : x, blk = y / D, z = y % D;
+    const uint32_t old = s_old[is_v][blk], now = s_new[is_v][blk];
+    const int64_t base = (from_block + blk) << 4, page = page_of(base);
+    if (page < 0) continue;
+    const int64_t in = base & (P - 1);
+    if (!is_v) {
+      const int r = z & 15, g = z >> 4;
+      const int64_t j = base + r - len;
+      const bool arrives = j >= 0 && j < count && s_moves[j];
+      if (!arrives && now == old) continue;
+      u32x4v* at = reinterpret_cast<u32x4v*>(c.k) + (page * head_bytes >> 4) + g * P + in + r;
+      *at = rescaled(arrives ? lk[j * gran + g] : *at, arrives ? s_from[0][j] : old, now);
+    } else {
+      u32x4v* at = reinterpret_cast<u32x4v*>(c.v) + (page * head_bytes >> 4) + (in >> 4) * D + z;
+      u32x4v v = *at;
+      if (now != old) v = rescaled(v, old, now);
+      for (int r = 0; r < 16; ++r) {
+        const int64_t j = base + r - len;
+        if (j < 0 || j >= count || !s_moves[j]) continue;
+        const int by = (r & 3) * 8;
+        const uint32_t code = rescaled4(lv[j * D + z], s_from[1][j], now) & 0xFFu;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) v[w] = r >> 2 == w ? (v[w] & ~(0xFFu << by)) | code << by : v[w];
+      }
+      *at = v;
+    }
+  }
+  for (int x = tid; x < 2 * blocks; x += 256) {
+    const int64_t at = (from_block + (x >> 1)) << 4, page = page_of(at);
+    const uint32_t now = s_new[x & 1][x >> 1];
+    if (page >= 0 && now != s_old[x & 1][x >> 1]) (x & 1 ? scales.v : scales.k)[scale_at(page, at)] = (uint8_t)now;
+  }
+}
+
 __global__ __launch_bounds__(kPlan) void accept_lengths_kernel(CacheArgs c, const int32_t* seq_ids, int n,
                                                                int max_path, const int32_t* counts,
                                                                int32_t* new_lengths) {
@@ -388,16 +495,31 @@ size_t cache_fork_workspace_bytes(const CacheArgs& c, int n) {
   return round256((size_t)n * sizeof(ForkEntry)) + round256((size_t)n * 4) + round256((size_t)n * (size_t)c.width * 4);
 }
 
-hipError_t launch_cache_fork(const CacheArgs& c, const int32_t* parents, const int32_t* children, int n,
-                             int32_t* granted, void* workspace, hipStream_t stream) {
+namespace {
+
+template <bool SCALED>
+hipError_t launch_fork(const CacheArgs& c, const Scales& s, const int32_t* parents, const int32_t* children, int n,
+                       int32_t* granted, void* workspace, hipStream_t stream) {
   char* w = reinterpret_cast<char*>(workspace);
   ForkEntry* entries = reinterpret_cast<ForkEntry*>(w);
   int32_t* list = reinterpret_cast<int32_t*>(w + round256((size_t)n * sizeof(ForkEntry)));
   int32_t* rows = reinterpret_cast<int32_t*>(w + round256((size_t)n * sizeof(ForkEntry)) + round256((size_t)n * 4));
   fork_snapshot_kernel<<<n, 256, 0, stream>>>(c, parents, children, entries, rows);
   fork_plan_kernel<<<1, kPlan, 0, stream>>>(c, n, entries, list);
-  fork_write_kernel<<<dim3(n, c.layers), 256, 0, stream>>>(c, children, entries, rows, granted);
+  fork_write_kernel<SCALED><<<dim3(n, c.layers), 256, 0, stream>>>(c, children, entries, rows, granted, s);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_cache_fork(const CacheArgs& c, const int32_t* parents, const int32_t* children, int n,
+                             int32_t* granted, void* workspace, hipStream_t stream) {
+  return launch_fork<false>(c, Scales{}, parents, children, n, granted, workspace, stream);
+}
+
+hipError_t launch_cache_fork_kv8(const CacheArgs& c, const Scales& s, const int32_t* parents, const int32_t* children,
+                                 int n, int32_t* granted, void* workspace, hipStream_t stream) {
+  return launch_fork<true>(c, s, parents, children, n, granted, workspace, stream);
 }
 
 hipError_t launch_cache_accept(const CacheArgs& c, const int32_t* seq_ids, int n, const int32_t* path, int max_path,
@@ -406,6 +528,18 @@ hipError_t launch_cache_accept(const CacheArgs& c, const int32_t* seq_ids, int n
   const bool in_place = new_lengths == c.lengths;
   accept_kernel<<<dim3(n + !in_place, c.layers, c.heads), 256, lds, stream>>>(c, seq_ids, n, path, max_path, counts,
                                                                               new_lengths);
+  if (in_place)
+    accept_lengths_kernel<<<1, kPlan, 0, stream>>>(c, seq_ids, n, max_path, counts, new_lengths);
+  return hipGetLastError();
+}
+
+hipError_t launch_cache_accept_kv8(const CacheArgs& c, const Scales& s, const int32_t* seq_ids, int n,
+                                   const int32_t* path, int max_path, const int32_t* counts, int32_t* new_lengths,
+                                   hipStream_t stream) {
+  const size_t lds = (size_t)max_path * c.head_dim * 2;
+  const bool in_place = new_lengths == c.lengths;
+  accept_kv8_kernel<<<dim3(n + !in_place, c.layers, c.heads), 256, lds, stream>>>(c, s, seq_ids, n, path, max_path,
+                                                                                  counts, new_lengths);
   if (in_place)
     accept_lengths_kernel<<<1, kPlan, 0, stream>>>(c, seq_ids, n, max_path, counts, new_lengths);
   return hipGetLastError();

@@ -135,9 +135,16 @@ struct AttnArgs {
   float scale;
 };
 
+// The same over a cache held in 8 bits: k and v are bytes.
+struct Attn8Args : AttnArgs {
+  const uint8_t* k_scale;     // [pages, heads, P/16] exponents
+  const uint8_t* v_scale;
+};
+
 // Workspace of a call: filled into the args' part_* by launch_attention.
 size_t attention_workspace_bytes(const AttnArgs& a);
 hipError_t launch_attention(AttnArgs a, void* workspace, hipStream_t stream);
+hipError_t launch_attention_kv8(Attn8Args a, void* workspace, hipStream_t stream);
 
 struct QkNormRopeArgs {
   const uint16_t *q, *k, *v, *q_weight, *k_weight;
@@ -150,6 +157,12 @@ struct QkNormRopeArgs {
   float eps;
 };
 hipError_t launch_qk_norm_rope(const QkNormRopeArgs& a, hipStream_t stream);
+
+// k_cache and v_cache of the base are not used.
+struct QkNormRope8Args : QkNormRopeArgs {
+  uint8_t *k8, *v8, *k_scale, *v_scale;
+};
+hipError_t launch_qk_norm_rope_kv8(const QkNormRope8Args& a, hipStream_t stream);
 
 // Page operations.  table / lengths / refs are the cache's device state.
 struct CacheArgs {
@@ -170,5 +183,15 @@ size_t cache_fork_workspace_bytes(const CacheArgs& c, int n);
 hipError_t launch_cache_accept(const CacheArgs& c, const int32_t* seq_ids, int n, const int32_t* path, int max_path,
                                const int32_t* counts, int32_t* new_lengths, hipStream_t stream);
 hipError_t launch_cache_free(const CacheArgs& c, const int32_t* seq_ids, int n, hipStream_t stream);
+
+// The cache held in 8 bits: k and v of the CacheArgs are bytes.
+struct Scales {
+  uint8_t *k, *v;             // [layers, pages, heads, P/16]
+};
+hipError_t launch_cache_fork_kv8(const CacheArgs& c, const Scales& s, const int32_t* parents, const int32_t* children,
+                                 int n, int32_t* granted, void* workspace, hipStream_t stream);
+hipError_t launch_cache_accept_kv8(const CacheArgs& c, const Scales& s, const int32_t* seq_ids, int n,
+                                   const int32_t* path, int max_path, const int32_t* counts, int32_t* new_lengths,
+                                   hipStream_t stream);
 
 }  // namespace trellis

@@ -1,7 +1,7 @@
 // qk_norm_rope.hip -- RMS norm of every query and key head, rotation by
 // position, and the append of keys and values to the paged cache, one pass.
 #include "internal.hpp"
-#include "kv_common.hpp"
+#include "norm_rope.hpp"
 
 namespace trellis {
 namespace {
@@ -10,12 +10,7 @@ constexpr int kThreads = 256;
 constexpr int TB = 8;          // tokens of a workgroup
 constexpr uint32_t kXcds = 8;
 
-// y = x / sqrt(mean x^2 + eps) * w over a head, then, over the first `rotary`
-// dimensions, (a, b) -> (a cos t - b sin t, b cos t + a sin t) with
-// t = position * inv_freq[i]: pairs (i, i + rotary / 2), or (2 i, 2 i + 1) when
-// interleaved.  Everything is f32 and rounded once; the angle is f64, since a
-// far position times a frequency needs more than f32's 24 bits for a
-// fraction of a turn.
+// Norm and rotation (norm_rope.hpp) are f32 and rounded once.
 //
 // Bound by memory: every value is read once and written once.  A workgroup
 // takes TB tokens and a share of the heads; the angles of its tokens are
@@ -50,10 +45,8 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(QkNormRopeArgs a
 
   for (int x = tid; x < tokens * half; x += kThreads) {
     const int t = x / half, i = x - t * half;
-    double turns = (double)a.positions[first + t] * (double)a.inv_freq[i] * 0.15915494309189533577;    // 1 / (2 pi)
-    turns -= rint(turns);
     float s, c;
-    sincospif(2.0f * (float)turns, &s, &c);
+    turn(a.positions[first + t], a.inv_freq[i], c, s);
     s_cos[t][i] = c;
     s_sin[t][i] = s;
   }
@@ -96,46 +89,8 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(QkNormRopeArgs a
     const int hh = is_q ? h : h - a.heads_q;
     const uint16_t* src = (is_q ? a.q + tok * a.q_stride : a.k + tok * a.k_stride) + hh * D + d0;
     const uint16_t* weight = (is_q ? a.q_weight : a.k_weight) + d0;
-    const u32x4v raw = *reinterpret_cast<const u32x4v*>(src), wr = *reinterpret_cast<const u32x4v*>(weight);
-    float y[8], sum = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      y[e] = T::to_f32((uint16_t)(raw[e >> 1] >> (16 * (e & 1))));
-      sum += y[e] * y[e];
-    }
-#pragma unroll
-    for (int d = LANES / 2; d; d >>= 1) sum += __shfl_xor(sum, d);
-    const float inv = 1.0f / sqrtf(sum * (1.0f / D) + a.eps);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = y[e] * inv * T::to_f32((uint16_t)(wr[e >> 1] >> (16 * (e & 1))));
-    const float *cs = s_cos[t], *sn = s_sin[t];
-    if (PAIRS) {
-      if (d0 < a.rotary) {
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const float c = cs[(d0 + e) >> 1], s = sn[(d0 + e) >> 1];
-          const float lo = y[e] * c - y[e + 1] * s, hi = y[e + 1] * c + y[e] * s;
-          y[e] = lo;
-          y[e + 1] = hi;
-        }
-      }
-    } else {
-      // the partner of dimension d is d +- rotary / 2, a whole number of lanes
-      // away: its input and weight are read again (they are in the L1) rather
-      // than sent through LDS
-      if (d0 < a.rotary) {
-        const int away = d0 < half ? half : -half, i = d0 < half ? d0 : d0 - half;
-        const u32x4v pr = *reinterpret_cast<const u32x4v*>(src + away);
-        const u32x4v pw = *reinterpret_cast<const u32x4v*>(weight + away);
-        const float sign = d0 < half ? -1.0f : 1.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float other = T::to_f32((uint16_t)(pr[e >> 1] >> (16 * (e & 1)))) * inv *
-                              T::to_f32((uint16_t)(pw[e >> 1] >> (16 * (e & 1))));
-          y[e] = y[e] * cs[i + e] + sign * (other * sn[i + e]);
-        }
-      }
-    }
+    float y[8];
+    norm_rotate<T, D, PAIRS>(src, weight, d0, a.rotary, a.eps, s_cos[t], s_sin[t], y);
     u32x4v res;
 #pragma unroll
     for (int w = 0; w < 4; ++w) res[w] = T::pack(y[2 * w], y[2 * w + 1]);
