@@ -356,6 +356,69 @@ int trellis_probe_gateup_decode_free(const uint32_t* gcodes, const uint16_t* gsc
                                      int64_t C, int M, int k, int L, int T, void* stream);
 
 /*
+ * ---- low-rank adapters beside the projections -----------------------------
+ *
+ * Packed codes cannot take an adapter's update, so fine-tunes of a packed
+ * model are served beside it: every request's own low-rank product is added
+ * to what the shared projection gave.  These operators are this library's
+ * additions.
+ *
+ * trellis_lora_add -- for each target: out = y + scales[a] * B_a (A_a x).
+ * Entry e (of n) has the rows starts[e] .. starts[e+1]-1 and the adapter
+ * a = adapters[e]; a number outside 0..pool-1 (-1) is no adapter: out = y.
+ * Rows of no entry are not written.  All targets of a call share x and the
+ * adapters' numbering (a layer's projections of one input).
+ *   x        bf16 [M, C], rows x_stride elements apart (a multiple of 8), C a
+ *            multiple of 8 (else TRELLIS_EUNSUPPORTED)
+ *   targets  host array of 1..TRELLIS_LORA_MAX, each
+ *     a        bf16 [pool, rank, C];  b  bf16 [pool, R, rank]
+ *     y, out   [M, R] of y_dtype (TRELLIS_OUT_BF16 or TRELLIS_OUT_F32), rows
+ *              y_stride and out_stride elements apart (any; 16-byte aligned
+ *              rows are faster).  out may be y itself; else the two must not
+ *              overlap.  Targets' outs must not overlap.
+ *   starts   int32 [n+1] ascending;  adapters int32 [n];  scales f32 [pool]
+ *   rank     8, 16, 32 or 64 (others: TRELLIS_EUNSUPPORTED)
+ *   ranks    int32 [pool]: an adapter's own rank, 0..rank; what A and B hold
+ *            past it is not looked at.  NULL: rank everywhere.
+ * Products and sums are f32: A x is kept to its 24 bits for the second
+ * product, and y + ... is rounded once, to y_dtype.  M = 0 is no work.
+ *
+ * trellis_lora_swiglu -- out = silu(g) * u, g = gate.y + its adapter's part,
+ * u = up.y + its: the gated activation of a layer whose gate and up
+ * projections have adapters, all in f32 and rounded once to bf16 (y_dtype
+ * f32: the raw sums of trellis_gateup_swiglu).  gate and up have the same R;
+ * their out fields are not read.  out bf16 [M, R], rows out_stride elements
+ * apart, may be gate.y or up.y where those are bf16.  Entries without an
+ * adapter give silu(gate.y) * up.y.
+ *
+ * The workspace holds A x: its size query takes the number of targets
+ * (swiglu: 2).
+ */
+#define TRELLIS_LORA_MAX 4
+/* Most rows of a call, and most outputs of a matrix (the launches' grids). */
+#define TRELLIS_LORA_MAX_ROWS 4194304
+#define TRELLIS_LORA_MAX_OUTPUTS 262144
+
+typedef struct trellis_lora_target {
+  const uint16_t* a;
+  const uint16_t* b;
+  const void* y;
+  void* out;
+  int64_t R, y_stride, out_stride;
+} trellis_lora_target;
+
+size_t trellis_lora_workspace_bytes(int64_t M, int64_t C, int n, int n_targets, int rank);
+int trellis_lora_add(const uint16_t* x, int64_t x_stride, const trellis_lora_target* targets, int n_targets,
+                     int y_dtype, const int32_t* starts, const int32_t* adapters, int n, const float* scales,
+                     const int32_t* ranks, int64_t pool, int rank, int64_t M, int64_t C, void* workspace,
+                     size_t workspace_bytes, void* stream);
+int trellis_lora_swiglu(const uint16_t* x, int64_t x_stride, const trellis_lora_target* gate,
+                        const trellis_lora_target* up, uint16_t* out, int64_t out_stride, int y_dtype,
+                        const int32_t* starts, const int32_t* adapters, int n, const float* scales,
+                        const int32_t* ranks, int64_t pool, int rank, int64_t M, int64_t C, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
  * ---- attention between the projections ------------------------------------
  *
  * A decoder layer's projections leave queries, keys and values; the calls

@@ -19,6 +19,9 @@ Attention between the projections (one paged key/value cache):
   table    int32 [seqs, width] page numbers, -1: none
   lengths  int32 [seqs] cached tokens;  refs  int32 [pages] holders of a page
 
+Low-rank adapters beside the projections:
+  a  bfloat16 [pool, rank, in];  b  bfloat16 [pool, out, rank]
+
 The same over a cache held in 8 bits (calls ending in _kv8):
   k_cache  float8_e4m3fn [(layers,) pages, kv_heads, D/16, P, 16]
   v_cache  float8_e4m3fn [(layers,) pages, kv_heads, P/16, D, 16]
@@ -41,6 +44,7 @@ KV_BF16, KV_F16 = 0, 1
 TREE_MAX = 64
 ACCEPT_MAX = 64
 CACHE_MAX_SEQS = 1024
+LORA_MAX = 4
 
 # every symbol include/trellis.h declares
 EXPORTS = (
@@ -62,6 +66,7 @@ EXPORTS = (
     "trellis_tree_attention_kv8_workspace_bytes", "trellis_tree_attention_kv8",
     "trellis_window_attention_kv8_workspace_bytes", "trellis_window_attention_kv8",
     "trellis_cache_fork_kv8_workspace_bytes", "trellis_cache_fork_kv8", "trellis_cache_accept_kv8",
+    "trellis_lora_workspace_bytes", "trellis_lora_add", "trellis_lora_swiglu",
     "trellis_decode_states", "trellis_last_error", "trellis_version",
 )
 
@@ -70,6 +75,12 @@ class TrellisError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"[status {status}] {msg}")
         self.status = status
+
+
+class LoraTarget(ctypes.Structure):
+    """trellis_lora_target of include/trellis.h"""
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("y", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("R", ctypes.c_int64), ("y_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
 
 
 class KvCache(ctypes.Structure):
@@ -167,6 +178,11 @@ def load_library():
             ("cache_fork", "_workspace_bytes", (_sz, [_vp, _vp, _int])),
             ("cache_fork", "", (_int, [_vp, _vp, _vp, _vp, _int, _vp, _vp, _sz, _vp])),
             ("cache_accept", "", (_int, [_vp, _vp, _vp, _int, _vp, _int, _vp, _vp, _vp])))},
+        "trellis_lora_workspace_bytes": (_sz, [_i64, _i64, _int, _int, _int]),
+        "trellis_lora_add": (_int, [_vp, _i64, _vp, _int, _int, _vp, _vp, _int, _vp, _vp, _i64, _int, _i64, _i64, _vp,
+                                    _sz, _vp]),
+        "trellis_lora_swiglu": (_int, [_vp, _i64, _vp, _vp, _vp, _i64, _int, _vp, _vp, _int, _vp, _vp, _i64, _int,
+                                       _i64, _i64, _vp, _sz, _vp]),
         "trellis_last_error": (ctypes.c_char_p, []),
         "trellis_version": (ctypes.c_char_p, []),
     }
@@ -924,3 +940,92 @@ def cache_free(table, lengths, refs, seq_ids):
     cache, state, dev = _state_only(table, lengths, refs, 16)
     ids = _tensor(seq_ids, "seq_ids", torch.int32, (None,), dev)
     _call(load_library().trellis_cache_free, dev, _byref(cache), _byref(state), ids, seq_ids.shape[0])
+
+
+# ---- low-rank adapters -----------------------------------------------------
+
+def _matrix_rows(t, name, shape, dtype, index):
+    """Address and row stride of [rows, n] whose rows may lie in a wider tensor; shape entries of None: any size."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    got = t.shape
+    if len(got) != 2 or any(w is not None and w != g for w, g in zip(shape, got)):
+        raise ValueError(f"{name}: shape {tuple(got)}, expected {tuple('any' if w is None else w for w in shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be a device tensor on the device of the call, is on {t.device}")
+    rows, n = got
+    if rows and n > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous, got strides {t.stride()}")
+    return t.data_ptr(), t.stride(0) if rows > 1 else n
+
+
+def _lora(x, a, b, ys, starts, adapters, scales, ranks):
+    """Checks what the two adapter calls share: (device number, x's address and stride, targets without their outs,
+    rank, pool, addresses of starts, adapters, scales and ranks, entries, the type of ys)."""
+    dev, bf16, i32 = _index(x, "x"), torch.bfloat16, torch.int32
+    xp, xs = _matrix_rows(x, "x", (None, None), bf16, dev)
+    M, C = x.shape
+    if not isinstance(a[0], torch.Tensor) or a[0].dim() != 3:
+        raise ValueError("a: expected [pool, rank, in]")
+    pool, rank, _ = a[0].shape
+    dt = ys[0].dtype if isinstance(ys[0], torch.Tensor) else None
+    if dt not in _F:
+        raise TypeError(f"y: dtype {dt} not in {_F}")
+    targets = []
+    for k, (ak, bk, y) in enumerate(zip(a, b, ys)):
+        ap = _tensor(ak, f"a[{k}]", bf16, (pool, rank, C), dev)
+        bp = _tensor(bk, f"b[{k}]", bf16, (pool, None, rank), dev)
+        yp, stride = _matrix_rows(y, f"ys[{k}]", (M, bk.shape[1]), dt, dev)
+        targets.append(LoraTarget(ap, bp, yp, None, bk.shape[1], stride, 0))
+    st = _tensor(starts, "starts", i32, (None,), dev)
+    n = starts.shape[0] - 1
+    ad = _tensor(adapters, "adapters", i32, (n,), dev)
+    sc = _tensor(scales, "scales", torch.float32, (pool,), dev)
+    rk = None if ranks is None else _tensor(ranks, "ranks", i32, (pool,), dev)
+    return dev, xp, xs, targets, rank, pool, st, ad, sc, rk, n, dt
+
+
+def lora_add(x, a, b, ys, starts, adapters, scales, ranks=None, outs=None, workspace=None):
+    """outs[k] = ys[k] + scales[i] * B_i (A_i x) for every row, i the adapter of the
+    row's entry: entry e has the rows starts[e] .. starts[e+1]-1 of x bf16 [M, C]
+    and adapter adapters[e] (-1: none, outs = ys).  a and b are lists of the
+    factors bf16 [pool, r, C] and [pool, R_k, r] of 1..4 projections of x, ys
+    their outputs [M, R_k] (bf16 or f32; views of a wider tensor may be given).
+    ranks int32 [pool]: adapters whose own rank is below r.  outs may be ys (in
+    place); rows of no entry are not written.  Returns outs."""
+    count = len(ys)
+    if not 1 <= count <= LORA_MAX or len(a) != count or len(b) != count:
+        raise ValueError(f"{len(a)} and {len(b)} factors for {count} projections (1..{LORA_MAX})")
+    dev, xp, xs, targets, rank, pool, st, ad, sc, rk, n, dt = _lora(x, a, b, ys, starts, adapters, scales, ranks)
+    M, C = x.shape
+    if outs is None:
+        outs = [torch.empty(y.shape, dtype=dt, device=y.device) for y in ys]
+    elif len(outs) != count:
+        raise ValueError(f"{len(outs)} outputs for {count} projections")
+    for k, (t, o) in enumerate(zip(targets, outs)):
+        t.out, t.out_stride = _matrix_rows(o, f"outs[{k}]", (M, t.R), dt, dev)
+    lib = load_library()
+    _keep, ws, wsb = _scratch(lib.trellis_lora_workspace_bytes(M, C, n, count, rank), x.device, workspace)
+    _call(lib.trellis_lora_add, dev, xp, xs, (LoraTarget * count)(*targets), count,
+          OUT_F32 if dt is torch.float32 else OUT_BF16, st, ad, n, sc, rk, pool, rank, M, C, ws, wsb)
+    return outs
+
+
+def lora_swiglu(x, a_gate, b_gate, a_up, b_up, gate, up, starts, adapters, scales, ranks=None, out=None,
+                workspace=None):
+    """bf16 silu(g) * u with g = gate + its adapter's part and u = up + its: gate and
+    up [M, R] (bf16 or f32, such as gate_f32 and up_f32 of gateup_swiglu); the
+    other arguments as lora_add.  Returns out [M, R]."""
+    dev, xp, xs, targets, rank, pool, st, ad, sc, rk, n, dt = _lora(x, (a_gate, a_up), (b_gate, b_up), (gate, up),
+                                                                    starts, adapters, scales, ranks)
+    M, C = x.shape
+    if out is None:
+        out = torch.empty((M, targets[0].R), dtype=torch.bfloat16, device=x.device)
+    op, stride = _matrix_rows(out, "out", (M, targets[0].R), torch.bfloat16, dev)
+    lib = load_library()
+    _keep, ws, wsb = _scratch(lib.trellis_lora_workspace_bytes(M, C, n, 2, rank), x.device, workspace)
+    _call(lib.trellis_lora_swiglu, dev, xp, xs, _byref(targets[0]), _byref(targets[1]), op, stride,
+          OUT_F32 if dt is torch.float32 else OUT_BF16, st, ad, n, sc, rk, pool, rank, M, C, ws, wsb)
+    return out

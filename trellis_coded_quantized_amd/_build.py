@@ -15,7 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libtrellis.so")
 SOURCES = ["api.hip", "api_attention.hip", "attention.hip", "attention_kv8.hip", "qk_norm_rope.hip", "qk_norm_rope_kv8.hip",
-           "cache.hip", "axis1.hip", "axis0.hip", "expand.hip", "prefill.hip", "probe.hip"]
+           "cache.hip", "lora.hip", "api_lora.hip", "axis1.hip", "axis0.hip", "expand.hip", "prefill.hip", "probe.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 CFLAGS = [

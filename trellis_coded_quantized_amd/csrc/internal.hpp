@@ -95,6 +95,41 @@ hipError_t launch_prefill_fused(const uint32_t* codes, const uint16_t* scales, c
                                 uint16_t* out, int64_t R, int64_t C, int64_t M, int k,
                                 void* workspace, hipStream_t stream, int axis0 = 0, int interleave = 0);
 
+// ---- low-rank adapters ----------------------------------------------------
+
+struct LoraTarget {
+  const uint16_t *a, *b;      // [pool, r, C], [pool, R, r]
+  const void* y;
+  void* out;
+  int64_t R, y_stride, out_stride;
+  int in_place;               // out is y: rows without an adapter need no copy
+  int blocks;                 // column blocks of the second product
+};
+
+struct LoraArgs {
+  const uint16_t* x;
+  const int32_t *starts, *adapters, *ranks;   // ranks: NULL for r everywhere
+  const float* scales;
+  float* part;                // [splits, M, n * r]
+  int64_t x_stride, M, C;
+  LoraTarget target[4];
+  int n, r, entries, pool, f32, aligned;
+  // filled by launch_lora
+  int64_t chunk;
+  int splits, cols, blocks, bare;
+};
+
+// How a call is cut: row tiles, column chunks, bytes of the workspace.
+struct LoraPlan {
+  bool few;
+  int rows, splits;
+  int64_t slots, chunk;
+  size_t bytes;
+};
+LoraPlan lora_plan(int64_t M, int entries, int64_t C, int n, int r);
+// swiglu: targets 0 and 1 are gate and up, target 0's out receives the result
+hipError_t launch_lora(LoraArgs a, bool swiglu, hipStream_t stream);
+
 // ---- attention over the paged cache and its page operations --------------
 
 // Errors of the C entry points, wherever they are defined: set the thread's
