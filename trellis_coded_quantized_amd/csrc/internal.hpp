@@ -121,9 +121,9 @@ struct LoraArgs {
 
 // How a call is cut: row tiles, column chunks, bytes of the workspace.
 struct LoraPlan {
-  bool few;
-  int rows, splits;
-  int64_t slots, chunk;
+  bool few;                   // short entries
+  int splits;
+  int64_t shrink_slots, expand_slots, chunk;
   size_t bytes;
 };
 LoraPlan lora_plan(int64_t M, int entries, int64_t C, int n, int r);
