@@ -943,29 +943,37 @@ def cache_free(table, lengths, refs, seq_ids):
 
 
 # ---- low-rank adapters -----------------------------------------------------
+# As above, checks are one pass of plain comparisons: a call of three matrices
+# has fifteen tensors.
 
-def _matrix_rows(t, name, shape, dtype, index):
-    """Address and row stride of [rows, n] whose rows may lie in a wider tensor; shape entries of None: any size."""
+_NAMES = {n: tuple(f"{n}[{k}]" for k in range(LORA_MAX)) for n in ("a", "b", "ys", "outs")}
+_BF = torch.bfloat16
+
+
+def _matrix_rows(t, name, rows, n, dtype, index):
+    """Address and row stride of [rows, n] (None: any size) whose rows may lie in a wider tensor."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    got = t.shape
-    if len(got) != 2 or any(w is not None and w != g for w, g in zip(shape, got)):
-        raise ValueError(f"{name}: shape {tuple(got)}, expected {tuple('any' if w is None else w for w in shape)}")
+    shape = t.shape
+    if len(shape) != 2 or (rows is not None and (shape[0] != rows or shape[1] != n)):
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected "
+                         f"{('any', 'any') if rows is None else (rows, n)}")
     if t.get_device() != index:
         raise ValueError(f"{name} must be a device tensor on the device of the call, is on {t.device}")
-    rows, n = got
-    if rows and n > 1 and t.stride(1) != 1:
+    row, one = t.stride()
+    if one != 1 and shape[0] and shape[1] > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous, got strides {t.stride()}")
-    return t.data_ptr(), t.stride(0) if rows > 1 else n
+    return t.data_ptr(), row if shape[0] > 1 else shape[1]
 
 
 def _lora(x, a, b, ys, starts, adapters, scales, ranks):
-    """Checks what the two adapter calls share: (device number, x's address and stride, targets without their outs,
-    rank, pool, addresses of starts, adapters, scales and ranks, entries, the type of ys)."""
-    dev, bf16, i32 = _index(x, "x"), torch.bfloat16, torch.int32
-    xp, xs = _matrix_rows(x, "x", (None, None), bf16, dev)
+    """Checks what the two adapter calls share: (device number, x's address, stride, rows and columns, for every
+    target the addresses of a, b and y with its outputs and stride, rank, pool, addresses of starts, adapters,
+    scales and ranks, entries, the type of ys)."""
+    dev, i32 = _index(x, "x"), torch.int32
+    xp, xs = _matrix_rows(x, "x", None, None, _BF, dev)
     M, C = x.shape
     if not isinstance(a[0], torch.Tensor) or a[0].dim() != 3:
         raise ValueError("a: expected [pool, rank, in]")
@@ -974,17 +982,19 @@ def _lora(x, a, b, ys, starts, adapters, scales, ranks):
     if dt not in _F:
         raise TypeError(f"y: dtype {dt} not in {_F}")
     targets = []
-    for k, (ak, bk, y) in enumerate(zip(a, b, ys)):
-        ap = _tensor(ak, f"a[{k}]", bf16, (pool, rank, C), dev)
-        bp = _tensor(bk, f"b[{k}]", bf16, (pool, None, rank), dev)
-        yp, stride = _matrix_rows(y, f"ys[{k}]", (M, bk.shape[1]), dt, dev)
-        targets.append(LoraTarget(ap, bp, yp, None, bk.shape[1], stride, 0))
+    for k, y in enumerate(ys):
+        bk = b[k]
+        ap = _tensor(a[k], _NAMES["a"][k], _BF, (pool, rank, C), dev)
+        bp = _tensor(bk, _NAMES["b"][k], _BF, (pool, None, rank), dev)
+        R = bk.shape[1]
+        yp, stride = _matrix_rows(y, _NAMES["ys"][k], M, R, dt, dev)
+        targets.append((ap, bp, yp, R, stride))
     st = _tensor(starts, "starts", i32, (None,), dev)
     n = starts.shape[0] - 1
     ad = _tensor(adapters, "adapters", i32, (n,), dev)
     sc = _tensor(scales, "scales", torch.float32, (pool,), dev)
     rk = None if ranks is None else _tensor(ranks, "ranks", i32, (pool,), dev)
-    return dev, xp, xs, targets, rank, pool, st, ad, sc, rk, n, dt
+    return dev, xp, xs, M, C, targets, rank, pool, st, ad, sc, rk, n, dt
 
 
 def lora_add(x, a, b, ys, starts, adapters, scales, ranks=None, outs=None, workspace=None):
@@ -998,18 +1008,19 @@ def lora_add(x, a, b, ys, starts, adapters, scales, ranks=None, outs=None, works
     count = len(ys)
     if not 1 <= count <= LORA_MAX or len(a) != count or len(b) != count:
         raise ValueError(f"{len(a)} and {len(b)} factors for {count} projections (1..{LORA_MAX})")
-    dev, xp, xs, targets, rank, pool, st, ad, sc, rk, n, dt = _lora(x, a, b, ys, starts, adapters, scales, ranks)
-    M, C = x.shape
+    dev, xp, xs, M, C, targets, rank, pool, st, ad, sc, rk, n, dt = _lora(x, a, b, ys, starts, adapters, scales, ranks)
     if outs is None:
-        outs = [torch.empty(y.shape, dtype=dt, device=y.device) for y in ys]
+        outs = [torch.empty_like(y) if y.is_contiguous() else torch.empty(y.shape, dtype=dt, device=y.device) for y in ys]
     elif len(outs) != count:
         raise ValueError(f"{len(outs)} outputs for {count} projections")
-    for k, (t, o) in enumerate(zip(targets, outs)):
-        t.out, t.out_stride = _matrix_rows(o, f"outs[{k}]", (M, t.R), dt, dev)
+    packed = (LoraTarget * count)()
+    for k, (ap, bp, yp, R, stride) in enumerate(targets):
+        op, out_stride = _matrix_rows(outs[k], _NAMES["outs"][k], M, R, dt, dev)
+        packed[k] = (ap, bp, yp, op, R, stride, out_stride)
     lib = load_library()
     _keep, ws, wsb = _scratch(lib.trellis_lora_workspace_bytes(M, C, n, count, rank), x.device, workspace)
-    _call(lib.trellis_lora_add, dev, xp, xs, (LoraTarget * count)(*targets), count,
-          OUT_F32 if dt is torch.float32 else OUT_BF16, st, ad, n, sc, rk, pool, rank, M, C, ws, wsb)
+    _call(lib.trellis_lora_add, dev, xp, xs, packed, count, OUT_F32 if dt is torch.float32 else OUT_BF16, st, ad, n, sc,
+          rk, pool, rank, M, C, ws, wsb)
     return outs
 
 
@@ -1018,14 +1029,14 @@ def lora_swiglu(x, a_gate, b_gate, a_up, b_up, gate, up, starts, adapters, scale
     """bf16 silu(g) * u with g = gate + its adapter's part and u = up + its: gate and
     up [M, R] (bf16 or f32, such as gate_f32 and up_f32 of gateup_swiglu); the
     other arguments as lora_add.  Returns out [M, R]."""
-    dev, xp, xs, targets, rank, pool, st, ad, sc, rk, n, dt = _lora(x, (a_gate, a_up), (b_gate, b_up), (gate, up),
-                                                                    starts, adapters, scales, ranks)
-    M, C = x.shape
+    dev, xp, xs, M, C, targets, rank, pool, st, ad, sc, rk, n, dt = _lora(x, (a_gate, a_up), (b_gate, b_up), (gate, up),
+                                                                          starts, adapters, scales, ranks)
+    gate_t, up_t = (LoraTarget(ap, bp, yp, None, R, stride, 0) for ap, bp, yp, R, stride in targets)
     if out is None:
-        out = torch.empty((M, targets[0].R), dtype=torch.bfloat16, device=x.device)
-    op, stride = _matrix_rows(out, "out", (M, targets[0].R), torch.bfloat16, dev)
+        out = torch.empty((M, gate_t.R), dtype=_BF, device=x.device)
+    op, out_stride = _matrix_rows(out, "out", M, gate_t.R, _BF, dev)
     lib = load_library()
     _keep, ws, wsb = _scratch(lib.trellis_lora_workspace_bytes(M, C, n, 2, rank), x.device, workspace)
-    _call(lib.trellis_lora_swiglu, dev, xp, xs, _byref(targets[0]), _byref(targets[1]), op, stride,
+    _call(lib.trellis_lora_swiglu, dev, xp, xs, _byref(gate_t), _byref(up_t), op, out_stride,
           OUT_F32 if dt is torch.float32 else OUT_BF16, st, ad, n, sc, rk, pool, rank, M, C, ws, wsb)
     return out

@@ -67,19 +67,19 @@ int run(const char* fn, bool swiglu, const uint16_t* x, int64_t x_stride, const 
   if (M == 0) return trellis::api_ok();
   const size_t size = y_dtype == TRELLIS_OUT_F32 ? 4 : 2, out_size = swiglu ? 2 : size;
   trellis::LoraArgs a{};
-  a.aligned = 1;
+  a.whole = 1;
   for (int k = 0; k < n_targets; ++k) {
     const trellis_lora_target& t = targets[k];
     TRY(check_matrix(fn, t, y_dtype));
     a.target[k] = trellis::LoraTarget{t.a, t.b, t.y, t.out, t.R, t.y_stride, t.out_stride, 0, 0};
-    a.aligned &= aligned_rows(t.y, t.y_stride, size);
+    a.whole &= t.R % 8 == 0 && aligned_rows(t.y, t.y_stride, size);
     if (swiglu && k) continue;                               // target 0's out is the call's
     TRY(need_ptr(fn, "out", t.out, out_size));
     if (t.out_stride < t.R) return api_fail(TRELLIS_EINVAL, "%s: out_stride=%lld below R", fn, (long long)t.out_stride);
     if (!swiglu && t.out == t.y && t.out_stride != t.y_stride)
       return api_fail(TRELLIS_EINVAL, "%s: out is y with another stride", fn);
     a.target[k].in_place = !swiglu && t.out == t.y;
-    a.aligned &= aligned_rows(t.out, t.out_stride, out_size);
+    a.whole &= aligned_rows(t.out, t.out_stride, out_size);
   }
   TRY(need_ptr(fn, "x", x, 16));
   TRY(need_ptr(fn, "starts", starts, 4));

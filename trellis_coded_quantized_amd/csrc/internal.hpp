@@ -113,10 +113,11 @@ struct LoraArgs {
   float* part;                // [splits, M, n * r]
   int64_t x_stride, M, C;
   LoraTarget target[4];
-  int n, r, entries, pool, f32, aligned;
+  int n, r, entries, pool, f32;
+  int whole;                  // y and out: rows 16-byte aligned, whole granules of eight
   // filled by launch_lora
   int64_t chunk;
-  int splits, cols, blocks, bare;
+  int first_target, splits, cols, blocks, slots, bare;
 };
 
 // How a call is cut: row tiles, column chunks, bytes of the workspace.
