@@ -236,7 +236,7 @@ __global__ __launch_bounds__(kThreads, 2) void lora_expand_kernel(LoraArgs a) {
   constexpr int R = NB * 8, G = SWIGLU ? 2 : 1, ROWS = MT * 16, STEP = SUB * 32 * kWaves;
   constexpr int E = 16 / sizeof(Y), ITEMS = 32 / E, Q = 16 * ITEMS / 64;      // outputs of a lane's item, items a row, a lane
   __shared__ __align__(16) uint16_t s_t[G][PARTS][ROWS][R + 8];               // padded: rows on different banks
-  __shared__ __align__(16) float s_part[kWaves][G][16][32 + 4];
+  __shared__ __align__(16) float s_part[kWaves][16][32 + 4];
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 15, grp = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // Workgroups of an XCD (every eighth) take neighbouring units, row tiles
@@ -259,8 +259,10 @@ __global__ __launch_bounds__(kThreads, 2) void lora_expand_kernel(LoraArgs a) {
   // item q of this lane: row of a tile, first output of a block
   auto item_row = [&](int q) { return (q * 64 + lane) / ITEMS; };
   const int item_at = lane % ITEMS * E;
-  u32x4v b[G][SUB][U::OPERANDS][2], y[G][SUB][MT][Q];
-  auto load = [&]() __attribute__((always_inline)) {
+  struct Ahead {
+    u32x4v b[G][SUB][U::OPERANDS][2], y[G][SUB][MT][Q];
+  };
+  auto load = [&](Ahead& to, int64_t c) __attribute__((always_inline)) {
 #pragma unroll
     for (int g = 0; g < G; ++g)
 #pragma unroll
@@ -271,7 +273,7 @@ __global__ __launch_bounds__(kThreads, 2) void lora_expand_kernel(LoraArgs a) {
           for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int q = 0; q < Q; ++q)
-              y[g][u][m][q] = *reinterpret_cast<const u32x4v*>(
+              to.y[g][u][m][q] = *reinterpret_cast<const u32x4v*>(
                   reinterpret_cast<const Y*>(target[g].y) +
                   (int64_t)(t.first + min(m * 16 + item_row(q), t.rows - 1)) * target[g].y_stride + i);
         }
@@ -282,13 +284,14 @@ __global__ __launch_bounds__(kThreads, 2) void lora_expand_kernel(LoraArgs a) {
             for (int z = 0; z < 2; ++z) {
               // what B holds past the adapter's rank is cut below; the address stays inside the matrix
               const int64_t i = min(c + u * 32 + (col >> 2) * 8 + z * 4 + (col & 3), out_n - 1);
-              b[g][u][q][z] = *reinterpret_cast<const u32x4v*>(target[g].b + ((int64_t)t.adapter * out_n + i) * R +
+              to.b[g][u][q][z] = *reinterpret_cast<const u32x4v*>(target[g].b + ((int64_t)t.adapter * out_n + i) * R +
                                                                U::block(q, grp) * 8);
             }
         }
       }
   };
-  load();
+  Ahead now, next;
+  load(now, c);
 
   u32x4v keep[U::OPERANDS];
   if (on) {
@@ -332,15 +335,16 @@ __global__ __launch_bounds__(kThreads, 2) void lora_expand_kernel(LoraArgs a) {
     }
   }
 
-  auto block_of = [&](const int u) __attribute__((always_inline)) {
+  auto block_of = [&](Ahead& from, int64_t c, const int u) __attribute__((always_inline)) {
     if (on)
 #pragma unroll
       for (int g = 0; g < G; ++g)
 #pragma unroll
-        for (int q = 0; q < U::OPERANDS; ++q) b[g][u][q][0] &= keep[q], b[g][u][q][1] &= keep[q];
+        for (int q = 0; q < U::OPERANDS; ++q) from.b[g][u][q][0] &= keep[q], from.b[g][u][q][1] &= keep[q];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       if (m * 16 >= t.rows) continue;
+      float d[Q][G][E] = {};
       if (on) {
 #pragma unroll
         for (int g = 0; g < G; ++g) {
@@ -351,62 +355,77 @@ __global__ __launch_bounds__(kThreads, 2) void lora_expand_kernel(LoraArgs a) {
             u32x4v v = *reinterpret_cast<const u32x4v*>(&s_t[g][part < PARTS ? part : 0][m * 16 + col][U::block(q, grp) * 8]);
             if (PARTS * NB % 4 && part >= PARTS) v = u32x4v{};               // units past the last part
 #pragma unroll
-            for (int z = 0; z < 2; ++z) acc[z] = mfma16(b[g][u][q % U::OPERANDS][z], v, acc[z]);
+            for (int z = 0; z < 2; ++z) acc[z] = mfma16(from.b[g][u][q % U::OPERANDS][z], v, acc[z]);
           }
 #pragma unroll
-          for (int z = 0; z < 2; ++z) *reinterpret_cast<f32x4v*>(&s_part[wave][g][col][grp * 8 + z * 4]) = acc[z];
+          for (int z = 0; z < 2; ++z) *reinterpret_cast<f32x4v*>(&s_part[wave][col][grp * 8 + z * 4]) = acc[z];
+          __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+#pragma unroll
+          for (int q = 0; q < Q; ++q)
+#pragma unroll
+            for (int e = 0; e < E; e += 4) {
+              const f32x4v w = *reinterpret_cast<const f32x4v*>(&s_part[wave][item_row(q)][item_at + e]);
+              d[q][g][e] = w[0], d[q][g][e + 1] = w[1], d[q][g][e + 2] = w[2], d[q][g][e + 3] = w[3];
+            }
+          __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
         }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
       }
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
         const int r = item_row(q);
-        float d[G][E] = {};
-        if (on)
-#pragma unroll
-          for (int g = 0; g < G; ++g)
-#pragma unroll
-            for (int e = 0; e < E; e += 4) {
-              const f32x4v w = *reinterpret_cast<const f32x4v*>(&s_part[wave][g][r][item_at + e]);
-              d[g][e] = w[0], d[g][e + 1] = w[1], d[g][e + 2] = w[2], d[g][e + 3] = w[3];
-            }
         const int64_t i = c + u * 32 + item_at, row = t.first + m * 16 + r;
         if (i < end && m * 16 + r < t.rows) {
           Out* out = reinterpret_cast<Out*>(target->out) + row * target->out_stride + i;
           if constexpr (WHOLE) {
             float v[E];
-            unpack(y[0][u][m][q], v);
+            unpack(from.y[0][u][m][q], v);
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[e] += d[0][e];
+            for (int e = 0; e < E; ++e) v[e] += d[q][0][e];
             if constexpr (SWIGLU) {
               float w[E];
-              unpack(y[G - 1][u][m][q], w);
+              unpack(from.y[G - 1][u][m][q], w);
 #pragma unroll
-              for (int e = 0; e < E; ++e) v[e] = silu_times(v[e], w[e] + d[G - 1][e]);
+              for (int e = 0; e < E; ++e) v[e] = silu_times(v[e], w[e] + d[q][G - 1][e]);
             }
             put(out, v);
           } else {
 #pragma unroll
             for (int e = 0; e < E; ++e)
               if (i + e < out_n) {
-                float v = get_one(reinterpret_cast<const Y*>(target->y) + row * target->y_stride + i + e) + d[0][e];
+                float v = get_one(reinterpret_cast<const Y*>(target->y) + row * target->y_stride + i + e) + d[q][0][e];
                 if constexpr (SWIGLU)
                   v = silu_times(v, get_one(reinterpret_cast<const Y*>(target[1].y) + row * target[1].y_stride + i + e) +
-                                        d[G - 1][e]);
+                                        d[q][G - 1][e]);
                 put_one(out + e, v);
               }
           }
         }
       }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
     }
   };
-  while (c < end) {
-    block_of(0);
-    if constexpr (SUB > 1) block_of(1);
-    if constexpr (SUB > 2) block_of(2), block_of(3);
-    c += STEP;
-    if (c < end) load();
+  auto work = [&](Ahead& from, int64_t c) __attribute__((always_inline)) {
+    block_of(from, c, 0);
+    if constexpr (SUB > 1) block_of(from, c, 1);
+    if constexpr (SUB > 2) block_of(from, c, 2), block_of(from, c, 3);
+  };
+  if constexpr (MT > 1 && !(SWIGLU && sizeof(Y) == 4 && NB == 8)) {
+    // the next loads are asked for before this step's stores: loads and stores
+    // are waited for in order
+    while (c < end) {
+      if (c + STEP < end) load(next, c + STEP);
+      work(now, c);
+      c += STEP;
+      if (c >= end) break;
+      if (c + STEP < end) load(now, c + STEP);
+      work(next, c);
+      c += STEP;
+    }
+  } else {
+    while (c < end) {
+      work(now, c);
+      c += STEP;
+      if (c < end) load(now, c);
+    }
   }
 }
 
@@ -506,7 +525,7 @@ hipError_t launch_lora(LoraArgs a, bool swiglu, hipStream_t stream) {
   // columns of a workgroup: as many as leave the compute units four workgroups
   int64_t all = 0;
   for (int k = 0; k < (swiglu ? 1 : a.n); ++k) all += a.target[k].R;
-  int64_t cols = p.expand_slots * all / (4 * (int64_t)device_cus());
+  int64_t cols = p.expand_slots * all / ((swiglu && !p.few ? 2 : 4) * (int64_t)device_cus());
   // short entries: four blocks a wave, or one
   const int unit = p.few && cols >= 3 * kCols ? 4 * kCols : kCols;
   a.cols = (int)(((cols < kCols ? kCols : cols > 4096 ? 4096 : cols) + unit - 1) / unit * unit);
