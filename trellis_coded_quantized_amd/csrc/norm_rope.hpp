@@ -18,13 +18,13 @@ __device__ __forceinline__ void turn(int32_t position, float inv_freq, float& c,
 // dimensions, (a, b) -> (a cos t - b sin t, b cos t + a sin t): pairs
 // (i, i + rotary / 2), or (2 i, 2 i + 1) when PAIRS.  The D / 8 lanes of a head
 // call it together, each with its eight dimensions from d0 on: src and weight
-// point at them, cs and sn at the token's angles.
+// point at them, raw is what src holds, cs and sn point at the token's angles.
 template <typename T, int D, bool PAIRS>
-__device__ __forceinline__ void norm_rotate(const uint16_t* src, const uint16_t* weight, int d0, int rotary, float eps,
-                                            const float* cs, const float* sn, float (&y)[8]) {
+__device__ __forceinline__ void norm_rotate(u32x4v raw, const uint16_t* src, const uint16_t* weight, int d0, int rotary,
+                                            float eps, const float* cs, const float* sn, float (&y)[8]) {
   constexpr int LANES = D / 8;
   const int half = rotary / 2;
-  const u32x4v raw = *reinterpret_cast<const u32x4v*>(src), wr = *reinterpret_cast<const u32x4v*>(weight);
+  const u32x4v wr = *reinterpret_cast<const u32x4v*>(weight);
   float sum = 0.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {

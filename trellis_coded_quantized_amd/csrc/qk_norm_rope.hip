@@ -90,7 +90,7 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(QkNormRopeArgs a
     const uint16_t* src = (is_q ? a.q + tok * a.q_stride : a.k + tok * a.k_stride) + hh * D + d0;
     const uint16_t* weight = (is_q ? a.q_weight : a.k_weight) + d0;
     float y[8];
-    norm_rotate<T, D, PAIRS>(src, weight, d0, a.rotary, a.eps, s_cos[t], s_sin[t], y);
+    norm_rotate<T, D, PAIRS>(*reinterpret_cast<const u32x4v*>(src), src, weight, d0, a.rotary, a.eps, s_cos[t], s_sin[t], y);
     u32x4v res;
 #pragma unroll
     for (int w = 0; w < 4; ++w) res[w] = T::pack(y[2 * w], y[2 * w + 1]);
