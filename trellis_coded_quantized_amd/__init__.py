@@ -1011,12 +1011,13 @@ def lora_add(x, a, b, ys, starts, adapters, scales, ranks=None, outs=None, works
     dev, xp, xs, M, C, targets, rank, pool, st, ad, sc, rk, n, dt = _lora(x, a, b, ys, starts, adapters, scales, ranks)
     if outs is None:
         outs = [torch.empty_like(y) if y.is_contiguous() else torch.empty(y.shape, dtype=dt, device=y.device) for y in ys]
+        to = [(o.data_ptr(), t[3]) for o, t in zip(outs, targets)]
     elif len(outs) != count:
         raise ValueError(f"{len(outs)} outputs for {count} projections")
-    packed = (LoraTarget * count)()
-    for k, (ap, bp, yp, R, stride) in enumerate(targets):
-        op, out_stride = _matrix_rows(outs[k], _NAMES["outs"][k], M, R, dt, dev)
-        packed[k] = (ap, bp, yp, op, R, stride, out_stride)
+    else:
+        to = [_matrix_rows(o, name, M, t[3], dt, dev) for o, name, t in zip(outs, _NAMES["outs"], targets)]
+    packed = (LoraTarget * count)(*[(ap, bp, yp, op, R, stride, out_stride)
+                                    for (ap, bp, yp, R, stride), (op, out_stride) in zip(targets, to)])
     lib = load_library()
     _keep, ws, wsb = _scratch(lib.trellis_lora_workspace_bytes(M, C, n, count, rank), x.device, workspace)
     _call(lib.trellis_lora_add, dev, xp, xs, packed, count, OUT_F32 if dt is torch.float32 else OUT_BF16, st, ad, n, sc,

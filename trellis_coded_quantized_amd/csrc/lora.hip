@@ -185,8 +185,17 @@ __global__ __launch_bounds__(kThreads, 2) void lora_shrink_kernel(LoraArgs a) {
 // eight ranks, four units a matrix instruction, and an operand of B serves all
 // parts.  MFMA row 4 g + e of instruction q is output 8 g + 4 q + e, so two
 // instructions leave eight neighbouring outputs of a row in a lane.
+//
+// 32 rows of B are one stretch of memory; they are loaded as that and turned
+// into operands in LDS, a wave's own: unit k of row i lies at k ^ turn(i), which
+// keeps the rows of an instruction on different banks.
 template <int NB, int PARTS>
 struct Units {
+  static constexpr int LOADS = NB < 2 ? 1 : NB / 2;          // of a wave, for 32 rows
+  static __device__ __forceinline__ int at(int i, int k) {
+    const int turn = NB == 8 ? (i >> 3) * 2 + ((i >> 1) & 1) : NB == 4 ? i >> 3 : NB == 2 ? (i >> 3) & 1 : 0;
+    return i * NB + (k ^ turn);
+  }
   static constexpr int MFMAS = (PARTS * NB + 3) / 4, OPERANDS = NB < 4 ? 1 : NB / 4;
   static __device__ __forceinline__ int block(int q, int grp) { return NB < 4 ? grp % NB : q % OPERANDS * 4 + grp; }
   static __device__ __forceinline__ int part(int q, int grp) { return (4 * q + grp) / NB; }
@@ -237,6 +246,7 @@ __global__ __launch_bounds__(kThreads, 2) void lora_expand_kernel(LoraArgs a) {
   constexpr int E = 16 / sizeof(Y), ITEMS = 32 / E, Q = 16 * ITEMS / 64;      // outputs of a lane's item, items a row, a lane
   __shared__ __align__(16) uint16_t s_t[G][PARTS][ROWS][R + 8];               // padded: rows on different banks
   __shared__ __align__(16) float s_part[kWaves][16][32 + 4];
+  __shared__ __align__(16) u32x4v s_b[kWaves][32 * NB];
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 15, grp = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // Workgroups of an XCD (every eighth) take neighbouring units, row tiles
@@ -260,7 +270,7 @@ __global__ __launch_bounds__(kThreads, 2) void lora_expand_kernel(LoraArgs a) {
   auto item_row = [&](int q) { return (q * 64 + lane) / ITEMS; };
   const int item_at = lane % ITEMS * E;
   struct Ahead {
-    u32x4v b[G][SUB][U::OPERANDS][2], y[G][SUB][MT][Q];
+    u32x4v b[G][SUB][U::LOADS], y[G][SUB][MT][Q];
   };
   auto load = [&](Ahead& to, int64_t c) __attribute__((always_inline)) {
 #pragma unroll
@@ -279,14 +289,11 @@ __global__ __launch_bounds__(kThreads, 2) void lora_expand_kernel(LoraArgs a) {
         }
         if (on) {
 #pragma unroll
-          for (int q = 0; q < U::OPERANDS; ++q)
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              // what B holds past the adapter's rank is cut below; the address stays inside the matrix
-              const int64_t i = min(c + u * 32 + (col >> 2) * 8 + z * 4 + (col & 3), out_n - 1);
-              to.b[g][u][q][z] = *reinterpret_cast<const u32x4v*>(target[g].b + ((int64_t)t.adapter * out_n + i) * R +
-                                                               U::block(q, grp) * 8);
-            }
+          for (int q = 0; q < U::LOADS; ++q) {
+            // what B holds past the adapter's rank is cut below; the address stays inside the matrix
+            const int64_t i = min(c + u * 32 + (q * 64 + lane) % (32 * NB) / NB, out_n - 1);
+            to.b[g][u][q] = *reinterpret_cast<const u32x4v*>(target[g].b + ((int64_t)t.adapter * out_n + i) * R + lane % NB * 8);
+          }
         }
       }
   };
@@ -336,11 +343,24 @@ __global__ __launch_bounds__(kThreads, 2) void lora_expand_kernel(LoraArgs a) {
   }
 
   auto block_of = [&](Ahead& from, int64_t c, const int u) __attribute__((always_inline)) {
-    if (on)
+    u32x4v b[G][U::OPERANDS][2];
+    if (on) {
 #pragma unroll
-      for (int g = 0; g < G; ++g)
+      for (int g = 0; g < G; ++g) {
 #pragma unroll
-        for (int q = 0; q < U::OPERANDS; ++q) from.b[g][u][q][0] &= keep[q], from.b[g][u][q][1] &= keep[q];
+        for (int q = 0; q < U::LOADS; ++q) {
+          const int unit = q * 64 + lane;
+          if (NB > 1 || unit < 32) s_b[wave][U::at(unit / NB, unit % NB)] = from.b[g][u][q];
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+#pragma unroll
+        for (int q = 0; q < U::OPERANDS; ++q)
+#pragma unroll
+          for (int z = 0; z < 2; ++z)
+            b[g][q][z] = s_b[wave][U::at((col >> 2) * 8 + z * 4 + (col & 3), U::block(q, grp))] & keep[q];
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+      }
+    }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       if (m * 16 >= t.rows) continue;
@@ -355,7 +375,7 @@ __global__ __launch_bounds__(kThreads, 2) void lora_expand_kernel(LoraArgs a) {
             u32x4v v = *reinterpret_cast<const u32x4v*>(&s_t[g][part < PARTS ? part : 0][m * 16 + col][U::block(q, grp) * 8]);
             if (PARTS * NB % 4 && part >= PARTS) v = u32x4v{};               // units past the last part
 #pragma unroll
-            for (int z = 0; z < 2; ++z) acc[z] = mfma16(from.b[g][u][q % U::OPERANDS][z], v, acc[z]);
+            for (int z = 0; z < 2; ++z) acc[z] = mfma16(b[g][q % U::OPERANDS][z], v, acc[z]);
           }
 #pragma unroll
           for (int z = 0; z < 2; ++z) *reinterpret_cast<f32x4v*>(&s_part[wave][col][grp * 8 + z * 4]) = acc[z];
@@ -408,7 +428,7 @@ __global__ __launch_bounds__(kThreads, 2) void lora_expand_kernel(LoraArgs a) {
     if constexpr (SUB > 1) block_of(from, c, 1);
     if constexpr (SUB > 2) block_of(from, c, 2), block_of(from, c, 3);
   };
-  if constexpr (MT > 1 && !(SWIGLU && sizeof(Y) == 4 && NB == 8)) {
+  if constexpr (MT > 1 && !(SWIGLU && sizeof(Y) == 4)) {     // there registers do not reach for two sets
     // the next loads are asked for before this step's stores: loads and stores
     // are waited for in order
     while (c < end) {
@@ -450,7 +470,7 @@ LoraPlan lora_plan(int64_t M, int entries, int64_t C, int n, int r) {
   if (splits > want) splits = want;
   if (splits > most) splits = most;
   if (splits < 1) splits = 1;
-  p.chunk = ((C + splits - 1) / splits + 255) / 256 * 256;           // whole steps of all waves
+  p.chunk = ((C + splits - 1) / splits + 127) / 128 * 128;           // whole steps of all waves
   p.splits = (int)((C + p.chunk - 1) / p.chunk);
   p.bytes = ((size_t)p.splits * (size_t)M * n * r * 4 + 255) / 256 * 256;
   return p;
@@ -489,7 +509,7 @@ void expand(const LoraArgs& a, const LoraPlan& p, hipStream_t stream) {
     kernel = p.few ? lora_expand_kernel<Y, NB, 1, 1, false, SWIGLU> : lora_expand_kernel<Y, NB, LONG, 1, false, SWIGLU>;
   else if (p.few)
     kernel = a.cols % (4 * kCols) ? lora_expand_kernel<Y, NB, 1, 1, true, SWIGLU>
-                                  : lora_expand_kernel<Y, NB, 1, 4, true, SWIGLU>;
+                                  : lora_expand_kernel<Y, NB, 1, SWIGLU && NB == 8 ? 2 : 4, true, SWIGLU>;
   kernel<<<grid, kThreads, 0, stream>>>(a);
 }
 
