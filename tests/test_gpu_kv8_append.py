@@ -120,6 +120,30 @@ def test_long_lists(N):
     w.check(w.run())
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("seed", range(8))
+def test_lists_of_any_kind(D, seed):
+    """Runs of any length at any place of a block, whole blocks, tokens that are not cached between them, and blocks
+    that are much quieter than what comes."""
+    g = torch.Generator().manual_seed(100 * seed + D)
+    pick = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=g))
+    P, pages = [16, 32, 64][seed % 3], 60
+    blocks = torch.randperm(pages * P // 16, generator=g).tolist()
+    slots = []
+    for _ in range(pick(1, 40)):
+        kind = pick(0, 3)
+        if kind == 0:
+            slots += [-1] * pick(1, 5)
+            continue
+        at = torch.randperm(16, generator=g)[:16 if kind == 1 else pick(1, 16) if kind == 2 else 1]
+        block = blocks.pop()
+        slots += [block * 16 + p for p in at.tolist()]
+    w = World(torch.tensor(slots, dtype=torch.int32), 2, 3, D, P, 32, [BF16, FP16][seed % 2], pages, seed=seed)
+    w.ks = torch.where(torch.rand(w.ks.shape, generator=g) < 0.3, torch.full_like(w.ks, 90), w.ks)
+    w.vs = torch.where(torch.rand(w.vs.shape, generator=g) < 0.3, torch.full_like(w.vs, 90), w.vs)
+    w.check(w.run())
+
+
 def test_tokens_of_a_block_in_any_order_and_with_gaps():
     slots = torch.tensor([16 * 5 + p for p in (9, 2, 14, 3)] + [16 * 2 + p for p in range(15, -1, -1)] +
                          [16 * 7 + p for p in (0, 4)] + [16 * 5 + 16], dtype=torch.int32)

@@ -101,6 +101,28 @@ def test_add(rank, dtype, counts, ids, C, Rs):
     c.check_add(tq.lora_add(*c.up()))
 
 
+@pytest.mark.parametrize("rank", [16, 64])
+@pytest.mark.parametrize("counts", [[1, 2], [100, 3]])
+def test_four_projections_of_unlike_widths(rank, counts):
+    c = Case(counts, [2, 0], 1024, [1024, 8, 264, 2048], rank, BF16, ranks=[rank, 3, rank - 5, 1, 1, 1], seed=rank)
+    c.check_add(tq.lora_add(*c.up(), **c.kw()))
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_lists_of_any_kind(seed):
+    """Entries from none to hundreds of rows, most of them short or most of them long, any ranks and widths."""
+    g = torch.Generator().manual_seed(seed)
+    pick = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=g))
+    entries, rank, pool = pick(1, 40), [8, 16, 32, 64][seed % 4], pick(1, 9)
+    counts = [pick(0, [1, 3, 40, 200][pick(0, 3)]) for _ in range(entries)]
+    ids = [pick(-1, pool) for _ in range(entries)]
+    Rs = [pick(1, 90) * [1, 8][pick(0, 1)] for _ in range(pick(1, 4))]
+    c = Case(counts, ids, 8 * pick(1, 100), Rs, rank, [BF16, F32][pick(0, 1)], pool=pool,
+             ranks=[pick(0, rank) for _ in range(pool)], first=pick(0, 5), after=pick(0, 5), seed=seed)
+    filled = [torch.full_like(y, 9.0) for y in c.up()[3]]
+    c.check_add(tq.lora_add(*c.up(), **c.kw(), outs=filled), before=[torch.full_like(y, 9.0) for y in c.y])
+
+
 @pytest.mark.parametrize("rank", [8, 16, 32, 64])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("counts,ids", [([1], [2]), ([3, 1, 2], [0, -1, 5]), ([70, 1, 130], [3, 9, 1])])
