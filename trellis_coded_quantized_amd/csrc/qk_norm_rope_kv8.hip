@@ -293,30 +293,26 @@ __device__ void keys_values(const QkNormRope8Args& a, int64_t first, int window,
       if (!grew) a.v8[s_run[r].values + (hb + h) * head_bytes + d * 16 + s_place[t]] = s_code[1][x];
     }
     // blocks whose scale grew: their other keys, and values as whole granules
-    for (int b = 0; grown && b < blocks; ++b) {
-      const int r = b / heads, h = b - r * heads;
+    for (int x = tid; grown && x < blocks * D; x += THREADS) {
+      const int b = x / D, y = x % D, r = b / heads, h = b - r * heads;
       const Run& run = s_run[r];
       if (run.places & 1u) continue;
-      uint8_t* const kd = a.k8 + run.keys + (hb + h) * head_bytes;
-      uint8_t* const vd = a.v8 + run.values + (hb + h) * head_bytes;
-      if (s_new[0][b] != s_old[0][b])
-        for (int x = tid; x < D; x += THREADS) {
-          if ((run.places >> (x & 15)) & 1) continue;
-          u32x4v* at = reinterpret_cast<u32x4v*>(kd + ((x >> 4) * P + (x & 15)) * 16);
-          *at = rescaled(*at, s_old[0][b], s_new[0][b]);
-        }
-      if (s_new[1][b] != s_old[1][b])
-        for (int d = tid; d < D; d += THREADS) {
-          u32x4v* at = reinterpret_cast<u32x4v*>(vd + d * 16);
-          u32x4v g = rescaled(*at, s_old[1][b], s_new[1][b]);
-          for (int t = run.first; t < run.first + run.n; ++t) {
-            const int off = s_place[t], by = (off & 3) * 8;
-            const uint32_t c = (uint32_t)s_code[1][(h * n + t) * D + d] << by, out = ~(0xFFu << by);
+      const uint32_t k0 = s_old[0][b], k1 = s_new[0][b], w0 = s_old[1][b], w1 = s_new[1][b];
+      if (k1 != k0 && !((run.places >> (y & 15)) & 1)) {
+        u32x4v* at = reinterpret_cast<u32x4v*>(a.k8 + run.keys + (hb + h) * head_bytes + ((y >> 4) * P + (y & 15)) * 16);
+        *at = rescaled(*at, k0, k1);
+      }
+      if (w1 != w0) {
+        u32x4v* at = reinterpret_cast<u32x4v*>(a.v8 + run.values + (hb + h) * head_bytes + y * 16);
+        u32x4v g = rescaled(*at, w0, w1);
+        for (int t = run.first; t < run.first + run.n; ++t) {
+          const int off = s_place[t], by = (off & 3) * 8;
+          const uint32_t c = (uint32_t)s_code[1][(h * n + t) * D + y] << by, out = ~(0xFFu << by);
 #pragma unroll
-            for (int w = 0; w < 4; ++w) g[w] = off >> 2 == w ? (g[w] & out) | c : g[w];
-          }
-          *at = g;
+          for (int w = 0; w < 4; ++w) g[w] = off >> 2 == w ? (g[w] & out) | c : g[w];
         }
+        *at = g;
+      }
     }
   }
 }
@@ -340,17 +336,24 @@ template <typename T, int D, bool PAIRS>
 hipError_t launch(const QkNormRope8Args& a, hipStream_t stream) {
   typedef Shape<D> S;
   const int cus = device_cus();
-  auto shared = [&](int64_t blocks, int64_t most) {          // until a compute unit has four workgroups
-    const int64_t s = 4 * (int64_t)cus / blocks;
+  auto shared = [](int64_t have, int64_t want, int64_t most) {
+    const int64_t s = want / have;
     return (int)(s > most ? most : s < 1 ? 1 : s);
   };
   const int64_t q_groups = (a.tokens + TB - 1) / TB;
   const int rounds = a.heads_q * TB * S::LANES / S::THREADS; // of a workgroup with all query heads
-  const int q_shares = shared(q_groups, rounds < 1 ? 1 : rounds > 64 ? 64 : rounds);
+  const int q_shares = shared(q_groups, 4 * cus, rounds < 1 ? 1 : rounds > 64 ? 64 : rounds);
   // few tokens: a workgroup each, which may find that its run began before
   const int window = a.tokens > 128 ? S::WINDOW : 1;
   const int64_t windows = (a.tokens + window - 1) / window;
-  const int kv_shares = shared(windows, a.heads_kv);
+  // Many windows: enough workgroups for 512 / D a compute unit (8191 tokens:
+  // 16 / 16 heads of 64 37 us with 2 shares a window, 30 with 4; 32 / 8 of 128
+  // 57 with 2, 70 with 1; 24 / 4 of 256 81 with 2, 66 with 1).  Few: a share a
+  // head, since the batches of a window take turns (300 tokens: 12.2 us with 8
+  // shares, 19.5 with 4); but where a window is one token, not fewer heads than
+  // fill a workgroup (64 tokens, 16 heads of 64: 6.6 us with 4, 9.7 with 16).
+  const int64_t most = window == 1 ? (a.heads_kv * 16 + S::UNITS - 1) / S::UNITS : a.heads_kv;
+  const int kv_shares = shared(windows, cus * (512 / D), most);
   const int64_t kv = windows * kv_shares, blocks = kv + q_groups * q_shares;
   if (blocks >= ((int64_t)1 << 31) / S::THREADS * 2) return hipErrorInvalidValue;
   qk_norm_rope_kv8_kernel<T, D, PAIRS><<<(unsigned)blocks, S::THREADS, 0, stream>>>(a, window, (int)kv, kv_shares, q_shares);
