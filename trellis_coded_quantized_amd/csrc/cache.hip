@@ -353,7 +353,8 @@ __global__ __launch_bounds__(256) void accept_kernel(CacheArgs c, const int32_t*
 // before any block changes; then a thread owns a granule of the blocks that
 // rows move into: it sets the rows that arrive and rounds the others again
 // where the block's scale grew.  The scales are written at the end, from what
-// all threads read at the start.
+// all threads read at the start.  A chain of latencies, as in 16 bits: 8 x 16
+// rows, 32 layers 10.6 us either way.
 constexpr int kAcceptBlocks = kCacheMaxPath / 16 + 1;
 __global__ __launch_bounds__(256) void accept_kv8_kernel(CacheArgs c, Scales scales, const int32_t* seq_ids, int n,
                                                          const int32_t* path, int max_path, const int32_t* counts,

@@ -4,6 +4,13 @@
 // The first product reads x and A once and leaves f32 partial sums of its
 // column chunks in the workspace; the second one adds them up, reads B and y
 // and writes y'.  Two launches: every output needs the whole of t.
+//
+// Bound by memory where entries are long: 8191 rows, 5120 -> 5120, rank 16,
+// 20.5 + 39 us traced, 5.2 and 4.6 TB/s of the copy's 5.1.  Gate and up of 5120
+// -> 17408 for 2047 rows, rank 64, in f32: 15 + 59 us (239 MB and 91 GFLOP
+// least), the second product's turns through LDS and its rounding beside the
+// loads; one adapter a row, 64 rows, rank 32, three matrices: 10 + 10 us, two
+// dependent launches over 45 MB.  One row: 4.5 + 4.8 us, latencies.
 #include "internal.hpp"
 #include "kv_common.hpp"
 #include <type_traits>
@@ -76,7 +83,8 @@ __device__ __forceinline__ f32x4v mfma16(u32x4v a, u32x4v b, f32x4v c) {
 // Operands have neighbouring lanes on neighbouring rows, C elements apart.
 // Loaded like that, every lane of 16 bytes is a request of its own to the L1
 // (counted: 63 of them a load; the second product, whose loads were like that,
-// was bound by them).  So a tile is loaded with neighbouring lanes along its
+// was bound by them: 2047 rows of gate and up 109 us then, 84 with both
+// products' loads along rows).  So a tile is loaded with neighbouring lanes along its
 // rows, and turned in LDS, a wave's own: granule g of row r lies at g ^ turn(r),
 // which keeps 16 rows' granules on different banks.  Its registers are free for
 // the next step's loads before this one's products run.
@@ -464,7 +472,8 @@ LoraPlan lora_plan(int64_t M, int entries, int64_t C, int n, int r) {
   p.expand_slots = slots_of(M, entries, p.few ? kShort : kLongExpand);
   // column chunks until the compute units have two workgroups, none shorter
   // than two steps of every wave.  Long entries: at most four, which every
-  // workgroup of the second product adds up again.
+  // workgroup of the second product adds up again (2047 rows of gate and up,
+  // 14 chunks: 364 us, four: 109).
   const int64_t want = 4 * (int64_t)device_cus() / (p.shrink_slots ? p.shrink_slots : 1), most = p.few ? 32 : 4;
   int64_t splits = (C + 255) / 256;
   if (splits > want) splits = want;

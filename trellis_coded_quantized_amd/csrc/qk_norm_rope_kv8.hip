@@ -323,7 +323,10 @@ __global__ __launch_bounds__(Shape<D>::THREADS, 4) void qk_norm_rope_kv8_kernel(
   __shared__ __align__(16) float s_cos[Shape<D>::MOST][D / 2], s_sin[Shape<D>::MOST][D / 2];
   // the two kinds in turn, so that queries' loads and stores go on while keys
   // and values wait at their barriers (8191 tokens, 32 / 8 heads of 128: one
-  // after the other in two launches 48 us, in turn 45)
+  // after the other in two launches 48 us, in turn 45; 185 MB at the copy's rate
+  // are 36).  Registers for more waves spill (96 of them: 59.5 against 56.1 us
+  // a call, 80: 73.6), and so do the next heads' loads ahead of this batch's
+  // stores (57 us either way, 256 dimensions 72 against 66).
   const uint64_t b = blockIdx.x;
   const int k = (int)(b * (uint64_t)kv_blocks / gridDim.x), q = (int)b - k;
   if ((int)((b + 1) * (uint64_t)kv_blocks / gridDim.x) > k)
