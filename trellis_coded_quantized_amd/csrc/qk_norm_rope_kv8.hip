@@ -278,7 +278,8 @@ __device__ void keys_values(const QkNormRope8Args& a, int64_t first, int window,
         for (int e = 0; e < 4; ++e) *reinterpret_cast<u32x4v*>(vd + h * head_bytes + (d + e) * 16) = g[e];
       }
     }
-    // new tokens of the others: granules of keys, bytes of values
+    // new tokens of the others: granules of keys, bytes of values (a lane has one
+    // dimension of all a run's tokens: 8 trees of 5 tokens 6.5 us, a byte a lane 7.6)
     const bool rest = full != (1u << runs) - 1;
     for (int x = tid; rest && x < units * (D / 16); x += THREADS) {
       const int u = x / (D / 16), g = x % (D / 16), h = head_of(u), t = u - h * n, r = s_of[t];
@@ -286,11 +287,13 @@ __device__ void keys_values(const QkNormRope8Args& a, int64_t first, int window,
       *reinterpret_cast<u32x4v*>(a.k8 + s_run[r].keys + (hb + h) * head_bytes + (g * P + s_place[t]) * 16) =
           *reinterpret_cast<const u32x4v*>(&s_code[0][x * 16]);
     }
-    for (int x = tid; rest && x < units * D; x += THREADS) {
-      const int u = x / D, d = x % D, h = head_of(u), t = u - h * n, r = s_of[t];
-      if (r < 0 || (full >> r) & 1) continue;
-      const bool grew = !(s_run[r].places & 1u) && s_new[1][r * heads + h] != s_old[1][r * heads + h];
-      if (!grew) a.v8[s_run[r].values + (hb + h) * head_bytes + d * 16 + s_place[t]] = s_code[1][x];
+    for (int x = tid; rest && x < blocks * D; x += THREADS) {
+      const int b = x / D, d = x % D, r = b / heads, h = b - r * heads;
+      const Run& run = s_run[r];
+      if ((full >> r) & 1 || (!(run.places & 1u) && s_new[1][b] != s_old[1][b])) continue;   // grew: below
+      uint8_t* const at = a.v8 + run.values + (hb + h) * head_bytes + d * 16;
+      const uint8_t* const code = &s_code[1][h * n * D + d];
+      for (int t = run.first, end = t + run.n; t < end; ++t) at[s_place[t]] = code[t * D];
     }
     // blocks whose scale grew: their other keys, and values as whole granules
     for (int x = tid; grown && x < blocks * D; x += THREADS) {
@@ -353,7 +356,7 @@ hipError_t launch(const QkNormRope8Args& a, hipStream_t stream) {
   // 16 / 16 heads of 64 37 us with 2 shares a window, 30 with 4; 32 / 8 of 128
   // 57 with 2, 70 with 1; 24 / 4 of 256 81 with 2, 66 with 1).  Few: a share a
   // head, since the batches of a window take turns (300 tokens: 12.2 us with 8
-  // shares, 19.5 with 4); but where a window is one token, not fewer heads than
+  // shares, 19.5 with 4, when tokens of open blocks were slower; 10.0 now); but where a window is one token, not fewer heads than
   // fill a workgroup (64 tokens, 16 heads of 64: 6.6 us with 4, 9.7 with 16).
   const int64_t most = window == 1 ? (a.heads_kv * 16 + S::UNITS - 1) / S::UNITS : a.heads_kv;
   const int kv_shares = shared(windows, cus * (512 / D), most);
