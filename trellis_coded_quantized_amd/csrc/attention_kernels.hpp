@@ -43,7 +43,7 @@ struct Kv16 {
 // kernel for few rows a lane half owns a block of keys:
 //   accumulator r of half h is key 16 h + r.
 // 64 single tokens over 16383 keys, 32 / 8 heads of 128: 222 + 5.5 us, 5.3 TB/s
-// of 1 byte an element; one over 200000: 75 + 5.6 us (the 16-bit cache: twice
+// of 1 byte an element; one over 200000, 24 / 4 of 256: 75 + 5.6 us (16 bits: twice
 // that).  Windows of 2047 x 3 tokens cost 239 us against 227 at 16 bits, 2 trees
 // of 64 over 131000 at D = 256 313 against 310: the conversions are vector work,
 // half as much is read.

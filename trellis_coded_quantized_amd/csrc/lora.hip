@@ -5,11 +5,11 @@
 // column chunks in the workspace; the second one adds them up, reads B and y
 // and writes y'.  Two launches: every output needs the whole of t.
 //
-// Bound by memory where entries are long: 8191 rows, 5120 -> 5120, rank 16,
-// 20.5 + 39 us traced, 5.2 and 4.6 TB/s of the copy's 5.1.  Gate and up of 5120
-// -> 17408 for 2047 rows, rank 64, in f32: 15 + 59 us (239 MB and 91 GFLOP
+// Bound by memory where entries are long: 8191 rows, 6144 -> 5120, rank 16,
+// 20.5 + 39 us traced, 5 and 4.5 TB/s of the copy's 5.1.  Gate and up of 5120
+// -> 17408 for 2047 rows, rank 64, bf16: 15 + 59 us (239 MB and 7.7 GFLOP
 // least), the second product's turns through LDS and its rounding beside the
-// loads; one adapter a row, 64 rows, rank 32, three matrices: 10 + 10 us, two
+// loads; 64 rows, 48 adapters of rank 32, three matrices: 10 + 10 us, two
 // dependent launches over 45 MB.  One row: 4.5 + 4.8 us, latencies.
 #include "internal.hpp"
 #include "kv_common.hpp"
@@ -23,7 +23,11 @@ constexpr unsigned kXcds = 8;
 constexpr int kCols = 32 * kWaves;    // columns that a workgroup's waves take at a time
 
 // Rows of one entry that a workgroup takes: one MFMA tile where entries are
-// short, two (first product) and four (second product) where they are long.
+// short, two (first product) and four (second product) where they are long:
+// gate and up of 2047 rows, rank 64, with 32 / 64 / 128 rows in the second
+// product 118 / 84 / 136 us (operands of B read for each tile; registers); tiles
+// of 16 rows in the first one 2 - 7 % faster up to 1024 rows, 1 - 8 % slower from
+// 2047 on.
 constexpr int kShort = 16, kLongShrink = 32, kLongExpand = 64;
 
 struct Tile {
