@@ -375,7 +375,8 @@ int trellis_probe_gateup_decode_free(const uint32_t* gcodes, const uint16_t* gsc
  *     y, out   [M, R] of y_dtype (TRELLIS_OUT_BF16 or TRELLIS_OUT_F32), rows
  *              y_stride and out_stride elements apart (any; 16-byte aligned
  *              rows are faster).  out may be y itself; else it must not
- *              overlap any target's y.  Targets' outs must not overlap.
+ *              overlap any target's y.  Targets' outs must not overlap.  x has
+ *              been read when the first output is written.
  *   starts   int32 [n+1] ascending;  adapters int32 [n];  scales f32 [pool]
  *   rank     8, 16, 32 or 64 (others: TRELLIS_EUNSUPPORTED)
  *   ranks    int32 [pool]: an adapter's own rank, 0..rank; what A and B hold

@@ -278,6 +278,34 @@ def test_other_stream_and_graph(counts):
         assert all(torch.equal(p, q) for p, q in zip(outs, eager))
 
 
+@pytest.mark.parametrize("counts", [[3, 70], [1, 1, 2]])
+def test_swiglu_into_its_up_and_add_into_x(counts):
+    c = Case(counts, [1, -1, 2][:len(counts)], 96, [96, 96], 16, BF16)
+    x, a, b, y, *rest = c.up()
+    want = tq.lora_swiglu(x, a[0], b[0], a[1], b[1], y[0], y[1], *rest)
+    got = tq.lora_swiglu(x, a[0], b[0], a[1], b[1], y[0], y[1], *rest, out=y[1])
+    assert torch.equal(got, want) and got is y[1]
+    (want,) = tq.lora_add(x, a[:1], b[:1], y[:1], *rest)
+    (got,) = tq.lora_add(x, a[:1], b[:1], y[:1], *rest, outs=[x])              # x has been read by then
+    assert torch.equal(got, want) and got is x
+
+
+def test_two_calls_at_once():
+    cases = [Case([90, 40], [1, 4], 512, [640, 32], 16, BF16, seed=1), Case([1] * 40, [0, 3] * 20, 512, [640, 32], 16, BF16, seed=2)]
+    args = [c.up() for c in cases]
+    want = [tq.lora_add(*t) for t in args]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for k, (t, side) in enumerate(zip(args, streams)):
+            with torch.cuda.stream(side):
+                got[k].append(tq.lora_add(*t))
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert all(torch.equal(p, q) for outs in got[k] for p, q in zip(outs, want[k]))
+
+
 def test_starts_outside_the_rows_touch_nothing_outside():
     c = Case([3, 4], [0, 1], 64, [16], 8, F32)
     x, a, b, y, _, adapters, scales = c.up()
