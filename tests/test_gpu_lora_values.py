@@ -1,0 +1,134 @@
+"""lora_add and lora_swiglu at the ends of their numbers: infinities in the
+factors, sums that need every bit of A x, numbers next to the largest."""
+import pytest
+import torch
+
+import trellis_coded_quantized_amd as tq
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+BF16, F32 = torch.bfloat16, torch.float32
+U = {BF16: 2.0 ** -8, F32: 2.0 ** -24}
+INF, NAN = float("inf"), float("nan")
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def pieces(t):
+    """f64 numbers of at most 24 bits -> three bf16 numbers that add up to each, along a new last dimension."""
+    out = []
+    for _ in range(3):
+        out.append(t.to(F32).to(BF16))
+        t = t - out[-1].double()
+    assert not t.any()
+    return torch.stack(out, -1)
+
+
+def exactly(t, rank):
+    """x bf16 [M, 8 M] and A [1, rank, 8 M] whose products A x are t [M, rank], rounded nowhere: row m has ones in
+    eight columns of its own, where A holds t's pieces."""
+    M = t.shape[0]
+    x, a = torch.zeros((M, 8 * M), dtype=BF16), torch.zeros((1, rank, 8 * M), dtype=BF16)
+    for m in range(M):
+        x[m, 8 * m:8 * m + 3] = 1
+        a[0, :, 8 * m:8 * m + 3] = pieces(t[m])
+    return x, a
+
+
+def add(x, a, b, y, scale=1.0, ranks=None):
+    out = tq.lora_add(x.to(DEV), [a.to(DEV)], [b.to(DEV)], [y.to(DEV)], ints([0, x.shape[0]]), ints([0]),
+                      torch.tensor([scale], device=DEV), ranks=None if ranks is None else ints(ranks))[0]
+    return out.cpu()
+
+
+def gated(x, a, b, gate, up, scale=1.0):
+    """Both projections have the same factors."""
+    a, b = a.to(DEV), b.to(DEV)
+    return tq.lora_swiglu(x.to(DEV), a, b, a, b, gate.to(DEV), up.to(DEV), ints([0, x.shape[0]]), ints([0]),
+                          torch.tensor([scale], device=DEV)).cpu()
+
+
+def agree(got, want, tol):
+    """The same infinities and NaN, the others within tol."""
+    got = got.double()
+    assert torch.equal(got.isnan(), want.isnan())
+    inf = want.isinf()
+    assert torch.equal(got[inf], want[inf])
+    rest = ~(inf | want.isnan())
+    assert not rest.any() or ((got - want).abs() - tol)[rest].max() <= 0
+
+
+# ---- infinities in B ------------------------------------------------------
+# t: on a bf16 number, above one, below one, above one by a second part that is
+# itself above a bf16 number, and zero
+T = [1.5, 1 + 2.0 ** -9, 1 - 2.0 ** -10, 1 + 2.0 ** -7 + 2.0 ** -9 + 2.0 ** -18, 0.0]
+
+
+@pytest.mark.parametrize("rank", [8, 16, 32, 64])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M", [5, 70])
+@pytest.mark.parametrize("R", [8, 200, 77])
+def test_infinite_entries_of_b(rank, dtype, M, R):
+    g = torch.Generator().manual_seed(rank + M + R)
+    at = torch.randint(0, len(T), (M, rank), generator=g)
+    t = torch.tensor(T, dtype=torch.float64)[at] * (torch.randint(0, 2, (M, rank), generator=g) * 2 - 1)
+    b = torch.randn((1, R, rank), generator=g).to(BF16)
+    for i in range(0, R, 3):                                   # rows of B with one infinity, two, or a NaN
+        for _ in range(1 + i % 2):
+            b[0, i, int(torch.randint(0, rank, (1,), generator=g))] = [INF, -INF, INF, NAN][i // 3 % 4]
+    y = torch.randn((M, R), generator=g).to(dtype)
+    x, a = exactly(t, rank)
+    d = (t[:, None] * b[0].double()).sum(-1)                   # a product for each, so that none hides another's NaN
+    # t enters with 16 bits at least, sums are f32
+    off = (t.abs()[:, None] * b[0].double().abs()).sum(-1) * (2.0 ** -17 + (3 * rank + 4) * 2.0 ** -24)
+    want = y.double() + d
+    agree(add(x, a, b, y), want, off + (U[dtype] + 2.0 ** -23) * want.abs())
+
+    up = torch.randn((M, R), generator=g).to(dtype)
+    gate = y.double() + d
+    silu, u = gate / (1 + torch.exp(-gate)), up.double() + d
+    want = silu * u
+    # |silu'| <= 1.1; the exponential's argument is rounded
+    tol = 1.1 * off * u.abs() + silu.abs() * off + 1.2 * off * off + (gate.abs() + 8) * 2.0 ** -22 * want.abs()
+    agree(gated(x, a, b, y, up), want, 1.01 * tol + U[BF16] * want.abs() + 1e-38)
+
+
+@pytest.mark.parametrize("rank", [8, 64])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_infinite_entries_of_b_beside_many_single_rows(rank, dtype):
+    """Wide outputs of many short entries, where a wave takes several blocks of columns."""
+    g = torch.Generator().manual_seed(rank)
+    M, R = 64, 8192
+    t = torch.tensor([[1 + 2.0 ** -9] * rank], dtype=torch.float64)
+    x, a = exactly(t, rank)
+    x = x.expand(M, -1).contiguous()
+    b = torch.randn((1, R, rank), generator=g).to(BF16)
+    bad = torch.randint(0, R, (R // 50,), generator=g)
+    b[0, bad, bad % rank] = INF
+    b[0, bad[::2], bad[::2] % rank] = -INF
+    starts, ids, s = ints(list(range(M + 1))), ints([0] * M), torch.ones(1, device=DEV)
+    y = torch.randn((M, R), generator=g).to(dtype)
+    d = (t * b[0].double()).sum(-1)
+    off = (t * b[0].double().abs()).sum(-1) * (2.0 ** -17 + (3 * rank + 4) * 2.0 ** -24)
+    want = y.double() + d
+    got = tq.lora_add(x.to(DEV), [a.to(DEV)], [b.to(DEV)], [y.to(DEV)], starts, ids, s)[0].cpu()
+    agree(got, want, off + (U[dtype] + 2.0 ** -23) * want.abs())
+    a, b, y = a.to(DEV), b.to(DEV), y.to(DEV)
+    got = tq.lora_swiglu(x.to(DEV), a, b, a, b, y, y, starts, ids, s).cpu()
+    silu = want / (1 + torch.exp(-want))
+    tol = (1.1 * want.abs() + silu.abs()) * off + 1.2 * off * off + (want.abs() + 8) * 2.0 ** -22 * (silu * want).abs()
+    agree(got, silu * want, 1.01 * tol + U[BF16] * (silu * want).abs() + 1e-38)
+
+
+def test_what_lies_past_a_rank_stays_out():
+    """NaN past the adapter's rank beside infinities within it."""
+    t = torch.tensor([[1 + 2.0 ** -9] * 16], dtype=torch.float64)
+    b = torch.ones((1, 40, 16), dtype=BF16)
+    b[0, ::2, 4], b[0, :, 5:] = INF, NAN
+    x, a = exactly(t, 16)
+    a[0, 5:] = NAN
+    out = add(x, a, b, torch.zeros((1, 40)), ranks=[5])
+    assert (out[0, ::2] == INF).all() and (out[0, 1::2] == 5 * (1 + 2.0 ** -9)).all()

@@ -201,6 +201,11 @@ __global__ __launch_bounds__(kThreads, 2) void lora_shrink_kernel(LoraArgs a) {
 // 32 rows of B are one stretch of memory; they are loaded as that and turned
 // into operands in LDS, a wave's own: unit k of row i lies at k ^ turn(i), which
 // keeps the rows of an instruction on different banks.
+//
+// Infinities and NaN of B meet the first part alone, which has t's sign: a
+// lower part is often zero or of the other sign, and inf * 0 and inf - inf are
+// NaN where B t is infinite.  Whether a wave's rows of B hold any is seen as
+// they enter LDS (64 rows, rank 64: 3 % of a call; others 1 %).
 template <int NB, int PARTS>
 struct Units {
   static constexpr int LOADS = NB < 2 ? 1 : NB / 2;          // of a wave, for 32 rows
@@ -212,6 +217,19 @@ struct Units {
   static __device__ __forceinline__ int block(int q, int grp) { return NB < 4 ? grp % NB : q % OPERANDS * 4 + grp; }
   static __device__ __forceinline__ int part(int q, int grp) { return (4 * q + grp) / NB; }
 };
+
+// The signs' places of two bf16 numbers, set where one is an infinity or NaN:
+// an exponent of all ones carries there when its last bit is added.
+__device__ __forceinline__ uint32_t nonfinite(uint32_t two) { return ((two & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+__device__ __forceinline__ bool any_nonfinite(u32x4v v) {
+  return (nonfinite(v[0]) | nonfinite(v[1]) | nonfinite(v[2]) | nonfinite(v[3])) != 0;
+}
+// the same numbers, those as zeros
+__device__ __forceinline__ u32x4v finite_ones(u32x4v v) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) v[w] &= ~((nonfinite(v[w]) >> 15) * 0xFFFFu);
+  return v;
+}
 
 __device__ __forceinline__ float silu_times(float g, float u) { return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u; }
 
@@ -356,12 +374,14 @@ __global__ __launch_bounds__(kThreads, 2) void lora_expand_kernel(LoraArgs a) {
 
   auto block_of = [&](Ahead& from, int64_t c, const int u) __attribute__((always_inline)) {
     u32x4v b[G][U::OPERANDS][2];
+    bool bad = false;                                        // infinities or NaN in these rows of B
     if (on) {
 #pragma unroll
       for (int g = 0; g < G; ++g) {
 #pragma unroll
         for (int q = 0; q < U::LOADS; ++q) {
           const int unit = q * 64 + lane;
+          bad |= any_nonfinite(from.b[g][u][q]);
           if (NB > 1 || unit < 32) s_b[wave][U::at(unit / NB, unit % NB)] = from.b[g][u][q];
         }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
@@ -372,6 +392,7 @@ __global__ __launch_bounds__(kThreads, 2) void lora_expand_kernel(LoraArgs a) {
             b[g][q][z] = s_b[wave][U::at((col >> 2) * 8 + z * 4 + (col & 3), U::block(q, grp))] & keep[q];
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
       }
+      bad = __any(bad);
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -381,14 +402,22 @@ __global__ __launch_bounds__(kThreads, 2) void lora_expand_kernel(LoraArgs a) {
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           f32x4v acc[2] = {};
+          auto product = [&](auto careful) __attribute__((always_inline)) {
 #pragma unroll
-          for (int q = 0; q < U::MFMAS; ++q) {
-            const int part = U::part(q, grp);
-            u32x4v v = *reinterpret_cast<const u32x4v*>(&s_t[g][part < PARTS ? part : 0][m * 16 + col][U::block(q, grp) * 8]);
-            if (PARTS * NB % 4 && part >= PARTS) v = u32x4v{};               // units past the last part
+            for (int q = 0; q < U::MFMAS; ++q) {
+              const int part = U::part(q, grp);
+              u32x4v v = *reinterpret_cast<const u32x4v*>(&s_t[g][part < PARTS ? part : 0][m * 16 + col][U::block(q, grp) * 8]);
+              if (PARTS * NB % 4 && part >= PARTS) v = u32x4v{};             // units past the last part
 #pragma unroll
-            for (int z = 0; z < 2; ++z) acc[z] = mfma16(b[g][q % U::OPERANDS][z], v, acc[z]);
-          }
+              for (int z = 0; z < 2; ++z) {
+                u32x4v w = b[g][q % U::OPERANDS][z];
+                if (careful && part > 0) w = finite_ones(w);
+                acc[z] = mfma16(w, v, acc[z]);
+              }
+            }
+          };
+          if (bad) product(std::true_type{});
+          else product(std::false_type{});
 #pragma unroll
           for (int z = 0; z < 2; ++z) *reinterpret_cast<f32x4v*>(&s_part[wave][col][grp * 8 + z * 4]) = acc[z];
           __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
