@@ -132,3 +132,36 @@ def test_what_lies_past_a_rank_stays_out():
     a[0, 5:] = NAN
     out = add(x, a, b, torch.zeros((1, 40)), ranks=[5])
     assert (out[0, ::2] == INF).all() and (out[0, 1::2] == 5 * (1 + 2.0 ** -9)).all()
+
+
+# ---- every bit of A x -----------------------------------------------------
+# Whole numbers below 2^24 in every sum, in any order: f32 is exact, and a bit
+# of t that is dropped shows where another rank or y takes the rest away.
+
+@pytest.mark.parametrize("rank", [8, 16, 32, 64])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M", [3, 70])
+@pytest.mark.parametrize("R", [24, 31])
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -8])
+def test_sums_that_cancel(rank, dtype, M, R, scale):
+    g = torch.Generator().manual_seed(rank + M + R)
+    t = torch.randint(-2 ** 22, 2 ** 22, (M, rank), generator=g).double()
+    t[:, 1::2] = t[:, ::2] + torch.randint(-300, 301, (M, rank // 2), generator=g)
+    b = torch.zeros((1, R, rank), dtype=BF16)                  # three ranks at most: two that cancel, and any one
+    for i in range(R):
+        j = int(torch.randint(0, rank // 2, (1,), generator=g)) * 2
+        b[0, i, j], b[0, i, j + 1] = 1, -1
+        if i % 3 == 2:
+            b[0, i, int(torch.randint(0, rank, (1,), generator=g))] = 1
+    x, a = exactly(t, rank)
+    d = t @ b[0].double().T * scale
+    y = (-d).to(dtype)
+    y[:, ::2] = 0
+    want = y.double() + d                                      # exact in f64, and in f32
+    assert torch.equal(want.float().double(), want)
+    assert torch.equal(add(x, a, b, y, scale), want.to(F32).to(dtype))
+    if scale < 1:
+        silu = want / (1 + torch.exp(-want))
+        tol = (want.abs() + 8) * 2.0 ** -22 + U[BF16]
+        keep = want > -80                                      # where the exponential is far from f32's end
+        agree(gated(x, a, b, y, y, scale)[keep], (silu * want)[keep], 1.01 * (tol * (silu * want).abs())[keep])

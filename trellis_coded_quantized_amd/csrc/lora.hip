@@ -191,9 +191,11 @@ __global__ __launch_bounds__(kThreads, 2) void lora_shrink_kernel(LoraArgs a) {
 }
 
 // ---- y + s B t -----------------------------------------------------------
-// t enters as PARTS bf16 numbers that add up to it: three make its 24 bits, for
-// f32 outputs, two make 16 and more (2^-17 of the adapter's share is far below
-// half a step of a bf16 output).  The contraction is (part, rank), in units of
+// t enters as three bf16 numbers, which hold its 24 bits.  Two hold 16, too few
+// for bf16 outputs also: where y or another rank's product cancels the rest,
+// the dropped bits are what is left (gate and up of 2047 rows, rank 64: 84.6 us
+// with two, 87.6 with three; 8191 rows, rank 16: 72.5 and 72.9).  The
+// contraction is (part, rank), in units of
 // eight ranks, four units a matrix instruction, and an operand of B serves all
 // parts.  MFMA row 4 g + e of instruction q is output 8 g + 4 q + e, so two
 // instructions leave eight neighbouring outputs of a row in a lane.
@@ -206,7 +208,9 @@ __global__ __launch_bounds__(kThreads, 2) void lora_shrink_kernel(LoraArgs a) {
 // lower part is often zero or of the other sign, and inf * 0 and inf - inf are
 // NaN where B t is infinite.  Whether a wave's rows of B hold any is seen as
 // they enter LDS (64 rows, rank 64: 3 % of a call; others 1 %).
-template <int NB, int PARTS>
+constexpr int PARTS = 3;
+
+template <int NB>
 struct Units {
   static constexpr int LOADS = NB < 2 ? 1 : NB / 2;          // of a wave, for 32 rows
   static __device__ __forceinline__ int at(int i, int k) {
@@ -269,8 +273,7 @@ __device__ __forceinline__ void put(uint16_t* p, const float (&v)[8]) {
 // SWIGLU: targets 0 and 1 are gate and up, outputs go to target 0's out.
 template <typename Y, int NB, int MT, int SUB, bool WHOLE, bool SWIGLU>
 __global__ __launch_bounds__(kThreads, 2) void lora_expand_kernel(LoraArgs a) {
-  constexpr int PARTS = SWIGLU || sizeof(Y) == 2 ? 2 : 3;
-  typedef Units<NB, PARTS> U;
+  typedef Units<NB> U;
   typedef typename std::conditional<SWIGLU, uint16_t, Y>::type Out;
   constexpr int R = NB * 8, G = SWIGLU ? 2 : 1, ROWS = MT * 16, STEP = SUB * 32 * kWaves;
   constexpr int E = 16 / sizeof(Y), ITEMS = 32 / E, Q = 16 * ITEMS / 64;      // outputs of a lane's item, items a row, a lane
