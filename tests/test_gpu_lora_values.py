@@ -165,3 +165,24 @@ def test_sums_that_cancel(rank, dtype, M, R, scale):
         tol = (want.abs() + 8) * 2.0 ** -22 + U[BF16]
         keep = want > -80                                      # where the exponential is far from f32's end
         agree(gated(x, a, b, y, y, scale)[keep], (silu * want)[keep], 1.01 * (tol * (silu * want).abs())[keep])
+
+
+@pytest.mark.parametrize("rank", [8, 64])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M", [2, 50])
+def test_finite_sums_past_the_largest_bf16(rank, dtype, M):
+    """A x = +-2^127 (2 - 2^-10) and neighbours, times small numbers: f32 holds all of it, bf16 only up to 2^127 (2 - 2^-8)."""
+    tops = torch.tensor([2 - 2.0 ** -7, 2 - 2.0 ** -8, 2 - 2.0 ** -10, 2 - 2.0 ** -23], dtype=torch.float64)
+    t = torch.zeros((M, rank), dtype=torch.float64)
+    t[:, rank - 2] = tops.repeat(M)[:M] * torch.tensor([1.0, 1, 1, 1, -1, -1, -1, -1]).repeat(M)[:M] * 2.0 ** 63
+    x = torch.zeros((M, 8 * M), dtype=BF16)
+    a = torch.zeros((1, rank, 8 * M), dtype=BF16)
+    for m in range(M):                                         # two pieces of at most 16 bits and one below
+        x[m, 8 * m:8 * m + 3] = 2.0 ** 64
+        one = t[m, rank - 2].clamp(-(2 - 2.0 ** -7) * 2.0 ** 63, (2 - 2.0 ** -7) * 2.0 ** 63)
+        a[0, rank - 2, 8 * m] = one
+        a[0, rank - 2, 8 * m + 1:8 * m + 3] = pieces(t[m, rank - 2] - one)[:2]
+    b = torch.zeros((1, 24, rank), dtype=BF16)
+    b[0, :, rank - 2] = 2.0 ** -torch.arange(4.0, 28.0)
+    want = t * 2.0 ** 64 @ b[0].double().T
+    assert torch.equal(add(x, a, b, torch.zeros((M, 24), dtype=dtype)), want.to(F32).to(dtype))

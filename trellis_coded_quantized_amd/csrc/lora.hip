@@ -222,6 +222,13 @@ struct Units {
   static __device__ __forceinline__ int part(int q, int grp) { return (4 * q + grp) / NB; }
 };
 
+// A finite number past bf16's largest becomes that, and the next part the rest;
+// rounded, it would be an infinity.
+__device__ __forceinline__ float within_bf16(float v) {
+  constexpr float kTop = 0x1.FEp127f;
+  return fabsf(v) < INFINITY ? fminf(fmaxf(v, -kTop), kTop) : v;
+}
+
 // The signs' places of two bf16 numbers, set where one is an infinity or NaN:
 // an exponent of all ones carries there when its last bit is added.
 __device__ __forceinline__ uint32_t nonfinite(uint32_t two) { return ((two & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
@@ -357,7 +364,10 @@ __global__ __launch_bounds__(kThreads, 2) void lora_expand_kernel(LoraArgs a) {
       for (int e = 0; e < 4; ++e) v[e] = j + e < t.rank ? v[e] * scale : 0.0f;
 #pragma unroll
       for (int p = 0; p < PARTS; ++p) {
-        const u32x2v w = {Bf16::pack(v[0], v[1]), Bf16::pack(v[2], v[3])};
+        float c[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[e] = p ? v[e] : within_bf16(v[e]);
+        const u32x2v w = {Bf16::pack(c[0], c[1]), Bf16::pack(c[2], c[3])};
         *reinterpret_cast<u32x2v*>(&s_t[g][p][m][j]) = w;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
