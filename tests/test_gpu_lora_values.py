@@ -186,3 +186,35 @@ def test_finite_sums_past_the_largest_bf16(rank, dtype, M):
     b[0, :, rank - 2] = 2.0 ** -torch.arange(4.0, 28.0)
     want = t * 2.0 ** 64 @ b[0].double().T
     assert torch.equal(add(x, a, b, torch.zeros((M, 24), dtype=dtype)), want.to(F32).to(dtype))
+
+
+# ---- the gated activation -------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M", [1, 70])
+@pytest.mark.parametrize("loud", [0, 60, 100])
+@pytest.mark.parametrize("R", [512, 509])
+def test_gates_far_below_zero(dtype, M, loud, R):
+    """-60 to -130: e^-g passes the end of f32, g / (1 + e^-g) times an up of 2^loud does not reach zero, or is a
+    subnormal number."""
+    g = torch.Generator().manual_seed(loud + M)
+    gate = (-60 - 70 * torch.rand((M, R), generator=g)).to(dtype)
+    up = (torch.randn((M, R), generator=g) * 2.0 ** loud).to(dtype)
+    x, a, b = torch.zeros((M, 8), dtype=BF16), torch.zeros((1, 8, 8), dtype=BF16), torch.zeros((1, R, 8), dtype=BF16)
+    want = gate.double() / (1 + torch.exp(-gate.double())) * up.double()
+    # the exponential's argument is rounded; half a step of bf16, of its subnormals 2^-133, and a few of f32's 2^-149
+    tol = (U[BF16] + (gate.double().abs() + 8) * 2.0 ** -22) * want.abs() + 2.0 ** -134 + 2.0 ** -146
+    agree(gated(x, a, b, gate, up), want, tol)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gates_of_any_size(dtype):
+    gate = torch.tensor([[0.0, -0.0, 1e-30, -1e-30, 1e30, -1e30, 88.0, -88.0, 300.0, -300.0, INF, NAN, 3e38, -3e38]]).to(dtype)
+    x, a = torch.zeros((1, 8), dtype=BF16), torch.zeros((1, 8, 8), dtype=BF16)
+    b = torch.zeros((1, gate.shape[1], 8), dtype=BF16)
+    for size in (1.0, -3.0, 1e-20, 0.0):
+        up = torch.full_like(gate, size)
+        want = torch.nn.functional.silu(gate.double()) * up.double()
+        got = gated(x, a, b, gate, up)
+        tol = (U[BF16] + torch.minimum(gate.double().abs() + 8, torch.tensor(400.0)) * 2.0 ** -22) * want.abs() + 2.0 ** -133
+        agree(got, want.to(BF16).double(), tol + U[BF16] * want.abs())
