@@ -218,3 +218,20 @@ def test_gates_of_any_size(dtype):
         got = gated(x, a, b, gate, up)
         tol = (U[BF16] + torch.minimum(gate.double().abs() + 8, torch.tensor(400.0)) * 2.0 ** -22) * want.abs() + 2.0 ** -133
         agree(got, want.to(BF16).double(), tol + U[BF16] * want.abs())
+
+
+# ---- no adapter -----------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("counts", [[1, 2], [70, 30]])
+@pytest.mark.parametrize("R", [40, 33])
+def test_rows_without_an_adapter_keep_every_bit(dtype, counts, R):
+    """Zeros of either sign, subnormal numbers, infinities: out = y, beside an entry with an adapter."""
+    M = sum(counts)
+    y = torch.tensor([0.0, -0.0, 2.0 ** -133, -2.0 ** -133, INF, -INF, 1.5]).repeat(M * R)[:M * R].view(M, R).to(dtype)
+    x, a, b = torch.ones((M, 8), dtype=BF16), torch.ones((1, 8, 8), dtype=BF16), torch.ones((1, R, 8), dtype=BF16)
+    kind = torch.int16 if dtype is BF16 else torch.int32
+    for ids, rows in (([-1, 0], slice(0, counts[0])), ([-1, -1], slice(0, M)), ([0, 1], slice(counts[0], M))):
+        out = tq.lora_add(x.to(DEV), [a.to(DEV)], [b.to(DEV)], [y.to(DEV)], ints([0, counts[0], M]), ints(ids),
+                          torch.ones(1, device=DEV))[0].cpu()
+        assert torch.equal(out[rows].view(kind), y[rows].view(kind))

@@ -420,7 +420,9 @@ __global__ __launch_bounds__(kThreads, 2) void lora_expand_kernel(LoraArgs a) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       if (m * 16 >= t.rows) continue;
-      float d[Q][G][E] = {};
+      float d[Q][G][E];
+#pragma unroll
+      for (int x = 0; x < Q * G * E; ++x) d[x / (G * E)][x / E % G][x % E] = -0.0f;   // rows without an adapter: y + -0 is y
       if (on) {
 #pragma unroll
         for (int g = 0; g < G; ++g) {
