@@ -638,7 +638,13 @@ def _kv_cache(k_cache, v_cache, layered):
                    _KV[dtype]), index
 
 
-_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+# a torch without these types serves every other call
+_E4M3, _E8M0 = (getattr(torch, name, None) for name in ("float8_e4m3fn", "float8_e8m0fnu"))
+
+
+def _need_8_bit_types():
+    if _E4M3 is None or _E8M0 is None:
+        raise TypeError("the cache in 8 bits needs torch.float8_e4m3fn and torch.float8_e8m0fnu, which this torch lacks")
 
 
 def _type_of(q):
@@ -652,6 +658,7 @@ def _type_of(q):
 
 def _kv8_cache(k_cache, v_cache, k_scale, v_scale, dtype, layered):
     """(Kv8Cache of the pools and scales after checking that they are one cache, device number)."""
+    _need_8_bit_types()
     index = _index(k_cache, "k_cache")
     shape = k_cache.shape
     n = len(shape)
@@ -835,6 +842,8 @@ def kv_cache(layers, pages, heads, head_dim, page_size, dtype=torch.bfloat16, de
 
 def kv8_cache(layers, pages, heads, head_dim, page_size, device="cuda"):
     """Empty pools and scales (k_cache, v_cache, k_scale, v_scale) of `layers` layers in 8 bits; [i] is one layer."""
+    _need_8_bit_types()
+
     def zeros(dtype, *shape):
         return torch.zeros((layers, pages, heads) + shape, dtype=torch.uint8, device=device).view(dtype)
 
