@@ -235,3 +235,42 @@ def test_rows_without_an_adapter_keep_every_bit(dtype, counts, R):
         out = tq.lora_add(x.to(DEV), [a.to(DEV)], [b.to(DEV)], [y.to(DEV)], ints([0, counts[0], M]), ints(ids),
                           torch.ones(1, device=DEV))[0].cpu()
         assert torch.equal(out[rows].view(kind), y[rows].view(kind))
+
+
+# ---- lists of long and short entries ---------------------------------------
+
+@pytest.mark.parametrize("rank", [8, 16, 32, 64])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("more", [0, 1])
+def test_a_prompt_among_single_rows(rank, dtype, more):
+    """Means of 128 / rank rows, and one row more: single rows, none, and one entry with all the others."""
+    g = torch.Generator().manual_seed(rank + more)
+    entries, pool, C, R = 24, 5, 264, 136
+    M = 128 // rank * entries + more
+    counts = [1] * entries
+    counts[3], counts[7] = 0, M - (entries - 2)
+    ids = [i % (pool + 1) - 1 for i in range(entries)]
+    x, y = torch.randn((M, C), generator=g).to(BF16), torch.randn((M, R), generator=g).to(dtype)
+    a, b = torch.randn((pool, rank, C), generator=g).to(BF16), torch.randn((pool, R, rank), generator=g).to(BF16)
+    scales = torch.rand(pool, generator=g) + 0.5
+    starts = [0]
+    for n in counts:
+        starts.append(starts[-1] + n)
+    d, off = torch.zeros((M, R), dtype=torch.float64), torch.zeros((M, R), dtype=torch.float64)
+    for e, i in enumerate(ids):
+        if i < 0:
+            continue
+        rows, s = slice(starts[e], starts[e + 1]), scales[i].double()
+        d[rows] = s * (x[rows].double() @ a[i].double().T) @ b[i].double().T
+        # sums of C products and at most 32 chunks, the scale, and sums over 3 ranks
+        off[rows] = (s * (x[rows].double().abs() @ a[i].double().abs().T) @ b[i].double().abs().T *
+                     (C + 32 + 1 + 3 * rank + 4) * 2.0 ** -24)
+    args = [ints(starts), ints(ids), scales.to(DEV)]
+    want = y.double() + d
+    got = tq.lora_add(x.to(DEV), [a.to(DEV)], [b.to(DEV)], [y.to(DEV)], *args)[0].cpu()
+    agree(got, want, U[dtype] * want.abs() + (off + 2.0 ** -24 * want.abs()) * (1 + 2 * U[dtype]))
+    a, b = a.to(DEV), b.to(DEV)
+    got = tq.lora_swiglu(x.to(DEV), a, b, a, b, y.to(DEV), y.to(DEV), *args).cpu()
+    silu, off = want / (1 + torch.exp(-want)), off + 2.0 ** -24 * want.abs()
+    tol = (1.1 * want.abs() + silu.abs()) * off + 1.2 * off * off + (want.abs() + 8) * 2.0 ** -22 * (silu * want).abs()
+    agree(got, silu * want, 1.01 * tol + U[BF16] * (silu * want).abs() + 1e-38)

@@ -537,7 +537,20 @@ int64_t slots_of(int64_t M, int entries, int rows) {
 
 LoraPlan lora_plan(int64_t M, int entries, int64_t C, int n, int r) {
   LoraPlan p;
-  p.few = M <= (int64_t)kShort * entries;
+  // Short tiles read A and B once for 16 rows, in many column chunks; long ones
+  // keep what they read for more rows.  Which is faster turns with the mean of
+  // rows and with the rank, at about 16, 8, 4, 2 rows for 8, 16, 32, 64 (us, short
+  // / long tiles, 5120 -> 6144 + 1024 + 1024 in bf16):
+  //   rank 16, 256 entries of 1, 4, 8 rows: 34 / 53, 49 / 58, 56 / 64;
+  //            32 of 8, 16, 24: 16.6 / 16.5, 20.3 / 17.9, 24.6 / 20.4
+  //   rank 64, 16 of 1, 4, 8: 24.5 / 31.9, 27.9 / 31.6, 32.4 / 31.8
+  // and gate and up, 5120 -> 17408:
+  //   rank 16, 64 of 1, 8: 31 / 37, 40 / 43;  rank 64, 16 of 1, 2, 8: 28 / 31,
+  //   31 / 32, 69 / 33, but 64 of 1 84 / 68.
+  // A prompt among single tokens is cut as the mean says, which loses little:
+  // rank 16, 1000 + 255 x 1 56 / 63, 1000 + 63 x 1 30 / 29, 500 + 63 x 1 23 / 27;
+  // gate and up, rank 64, 4000 + 31 x 1 365 / 259, 500 + 255 x 1 292 / 349.
+  p.few = M * r <= 128 * (int64_t)entries;
   p.shrink_slots = slots_of(M, entries, p.few ? kShort : kLongShrink);
   p.expand_slots = slots_of(M, entries, p.few ? kShort : kLongExpand);
   // column chunks until the compute units have two workgroups, none shorter
