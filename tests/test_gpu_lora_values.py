@@ -96,6 +96,30 @@ def test_infinite_entries_of_b(rank, dtype, M, R):
     agree(gated(x, a, b, y, up), want, 1.01 * tol + U[BF16] * want.abs() + 1e-38)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M", [3, 70])
+def test_infinities_and_nan_of_a_and_y(dtype, M):
+    """A's reach the outputs through the ranks that hold them, y's stay where they are."""
+    g = torch.Generator().manual_seed(M)
+    x = torch.randint(-2, 3, (M, 32), generator=g).to(BF16)
+    a = torch.randint(-2, 3, (1, 8, 32), generator=g).to(BF16)
+    a[0, 1, 5], a[0, 3, 7], a[0, 6, 2] = INF, -INF, NAN
+    b = torch.zeros((1, 24, 8), dtype=BF16)
+    for i in range(24):                                        # one rank each: zeros of B meet what t has of others
+        b[0, i, i % 8] = 1 - 2 * (i // 8 % 2)
+    y = torch.randint(-3, 4, (M, 24), generator=g).to(dtype)
+    y[0, 1], y[1, 2], y[2, 3] = INF, NAN, -INF
+    # element by element: sums of products as they stand, infinities and NaN among them
+    t = (x.double()[:, None] * a[0].double()).sum(-1)
+    want = y.double() + (t[:, None] * b[0].double()).sum(-1)
+    agree(add(x, a, b, y), want, torch.zeros_like(want))
+    a[0, 6, 2] = 1
+    t = (x.double()[:, None] * a[0].double()).sum(-1)
+    want = y.double() + (t[:, None] * b[0].double()).sum(-1)
+    agree(add(x, a, b, y), want, torch.zeros_like(want))
+    agree(add(x, a, b, y, ranks=[1]), y.double() + t[:, :1] * b[0, :, 0].double(), torch.zeros_like(want))
+
+
 @pytest.mark.parametrize("rank", [8, 64])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_infinite_entries_of_b_beside_many_single_rows(rank, dtype):
