@@ -381,8 +381,10 @@ int trellis_probe_gateup_decode_free(const uint32_t* gcodes, const uint16_t* gsc
  *   rank     8, 16, 32 or 64 (others: TRELLIS_EUNSUPPORTED)
  *   ranks    int32 [pool]: an adapter's own rank, 0..rank; what A and B hold
  *            past it is not looked at.  NULL: rank everywhere.
- * Products and sums are f32: A x is kept to its 24 bits for the second
- * product, and y + ... is rounded once, to y_dtype.  M = 0 is no work.
+ * Products and sums are f32: A x is kept to its 24 bits (in steps of no less
+ * than 2^-133) for the second product, and y + ... is rounded once, to y_dtype.
+ * Infinities and NaN of x, A, B and y stay in their rows and outputs, as the
+ * formula has them.  M = 0 is no work.
  *
  * trellis_lora_swiglu -- out = silu(g) * u, g = gate.y + its adapter's part,
  * u = up.y + its: the gated activation of a layer whose gate and up
@@ -390,7 +392,9 @@ int trellis_probe_gateup_decode_free(const uint32_t* gcodes, const uint16_t* gsc
  * f32: the raw sums of trellis_gateup_swiglu).  gate and up have the same R;
  * their out fields are not read.  out bf16 [M, R], rows out_stride elements
  * apart, may be gate.y or up.y where those are bf16.  Entries without an
- * adapter give silu(gate.y) * up.y.
+ * adapter give silu(gate.y) * up.y, rounded once too: trellis_gateup_swiglu
+ * rounds gate, up, the sigmoid and silu to bf16 on the way, so a request of no
+ * adapter gets other low bits beside requests of adapters than from that call.
  *
  * The workspace holds A x: its size query takes the number of targets
  * (swiglu: 2).
@@ -631,6 +635,8 @@ int trellis_cache_free(const trellis_kv_cache* cache, const trellis_kv_state* st
  *   b' = max(b, need)    elsewhere; where that is more than b, the block's
  *                        other tokens are rounded again under b' (exact but
  *                        for codes that fall below e4m3's normal numbers)
+ * A scale does not shrink before its block begins anew: a rejected draft leaves
+ * it as large as the draft needed.
  * Infinities and NaN are stored as NaN and do not count for the scale.
  * Magnitudes above the largest number with 4 significant bits of the 16-bit
  * type (bf16 1.875 * 2^127, fp16 61440) are stored as that number.

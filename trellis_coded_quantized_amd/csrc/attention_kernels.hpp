@@ -42,11 +42,10 @@ struct Kv16 {
 // operands: 16 dimensions of a token, or the 16 tokens of a block, so in the
 // kernel for few rows a lane half owns a block of keys:
 //   accumulator r of half h is key 16 h + r.
-// 64 single tokens over 16383 keys, 32 / 8 heads of 128: 222 + 5.5 us, 5.3 TB/s
-// of 1 byte an element; one over 200000, 24 / 4 of 256: 75 + 5.6 us (16 bits: twice
-// that).  Windows of 2047 x 3 tokens cost 239 us against 227 at 16 bits, 2 trees
-// of 64 over 131000 at D = 256 313 against 310: the conversions are vector work,
-// half as much is read.
+// 64 single tokens over 16383 keys, 32 / 8 heads of 128: 228 us a call, 5.3 TB/s
+// of 1 byte an element, 422 at 16 bits; one over 200000, 24 / 4 of 256: 81 and 148.
+// Windows of 2047 x 3 tokens take 222 us in either, 2 trees of 64 over 131000 at
+// D = 256 312 against 321: the conversions are vector work, half as much is read.
 struct Kv8 {
   typedef Attn8Args Args;
   static constexpr int PACK = 2;

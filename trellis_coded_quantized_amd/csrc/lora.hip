@@ -6,11 +6,14 @@
 // and writes y'.  Two launches: every output needs the whole of t.
 //
 // Bound by memory where entries are long: 8191 rows, 6144 -> 5120, rank 16,
-// 20.5 + 39 us traced, 5 and 4.5 TB/s of the copy's 5.1.  Gate and up of 5120
-// -> 17408 for 2047 rows, rank 64, bf16: 15 + 59 us (239 MB and 7.7 GFLOP
-// least), the second product's turns through LDS and its rounding beside the
-// loads; 64 rows, 48 adapters of rank 32, three matrices: 10 + 10 us, two
-// dependent launches over 45 MB.  One row: 4.5 + 4.8 us, latencies.
+// 21 + 40 us traced, 4.8 and 4.2 TB/s of the copy's 5.1.  Gate and up of 5120
+// -> 17408 for 2047 rows, rank 64, bf16: 15 + 65 us (239 MB and 7.7 GFLOP
+// least); the second product has two workgroups a compute unit for its
+// registers and LDS, which wait 41 % of their time, while nothing is saturated
+// (vector issue 47 %, matrix units 18 %).  64 rows, 48 adapters of rank 32, three
+// matrices: 10 + 10 us over 45 MB; a wave has two or three steps of work behind
+// a chain of dependent loads (starts, adapter, rank).  One row: 4.7 + 5.5 us,
+// latencies.
 #include "internal.hpp"
 #include "kv_common.hpp"
 #include <type_traits>

@@ -13,7 +13,7 @@ constexpr int TB = 8;             // tokens of a workgroup that has queries
 // could not come back from e4m3 and a scale.
 template <typename T>
 __device__ __forceinline__ float type_top() {
-  return __builtin_bit_cast(float, sizeof(T) && T::kExp == 0x7F80u ? 0x7F700000u : 0x47700000u);   // 1.875 2^127, 61440
+  return __builtin_bit_cast(float, T::kExp == 0x7F80u ? 0x7F700000u : 0x47700000u);   // 1.875 2^127, 61440
 }
 
 // Infinities become NaN, magnitudes end at the type's top; returns the largest
@@ -327,9 +327,12 @@ __global__ __launch_bounds__(Shape<D>::THREADS, 4) void qk_norm_rope_kv8_kernel(
   // the two kinds in turn, so that queries' loads and stores go on while keys
   // and values wait at their barriers (8191 tokens, 32 / 8 heads of 128: one
   // after the other in two launches 48 us, in turn 45; 185 MB at the copy's rate
-  // are 36).  Registers for more waves spill (96 of them: 59.5 against 56.1 us
-  // a call, 80: 73.6), and so do the next heads' loads ahead of this batch's
-  // stores (57 us either way, 256 dimensions 72 against 66).
+  // are 36).  Bound by vector work: it issues in 80 % of the cycles (norms, angles,
+  // conversions and largest magnitudes, weights converted for every head).
+  // Registers for more waves spill (96 of them: 57.1 against 56.8 us in a graph,
+  // 68 against 63 at 256 dimensions, 28 against 26 at 64; 80: 71, 83, 44), and
+  // so do the next heads' loads ahead of this batch's stores (57 us either way,
+  // 256 dimensions 72 against 66).
   const uint64_t b = blockIdx.x;
   const int k = (int)(b * (uint64_t)kv_blocks / gridDim.x), q = (int)b - k;
   if ((int)((b + 1) * (uint64_t)kv_blocks / gridDim.x) > k)
@@ -349,7 +352,11 @@ hipError_t launch(const QkNormRope8Args& a, hipStream_t stream) {
   const int64_t q_groups = (a.tokens + TB - 1) / TB;
   const int rounds = a.heads_q * TB * S::LANES / S::THREADS; // of a workgroup with all query heads
   const int q_shares = shared(q_groups, 4 * cus, rounds < 1 ? 1 : rounds > 64 ? 64 : rounds);
-  // few tokens: a workgroup each, which may find that its run began before
+  // Few tokens: a workgroup each, which may find that its run began before.  Of
+  // 32 / 8 heads of 128 (a workgroup each / 16 together, us): 64 single tokens
+  // 6.8 / 9.3, 128 7.8 / 10.0, 192 10.0 / 10.4, 256 11.9 / 11.3; one of 64 8.6 / 9.7,
+  // 160 9.8 / 9.7, 256 11.9 / 9.9, 512 20 / 11; heads of 64 even out at 128 already
+  // (7.9 / 7.7), 8 / 1 of 128 past 512.
   const int window = a.tokens > 128 ? S::WINDOW : 1;
   const int64_t windows = (a.tokens + window - 1) / window;
   // Many windows: enough workgroups for 512 / D a compute unit (8191 tokens:
