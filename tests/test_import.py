@@ -9,7 +9,7 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 CODE = """
 import torch
-del torch.{name}
+torch.__dict__.pop("{name}", None)
 import trellis_coded_quantized_amd as tq
 tq.load_library()
 assert callable(tq.matvec_axis1) and callable(tq.kv_cache)

@@ -28,9 +28,10 @@ constexpr int kCols = 32 * kWaves;    // columns that a workgroup's waves take a
 // Rows of one entry that a workgroup takes: one MFMA tile where entries are
 // short, two (first product) and four (second product) where they are long:
 // gate and up of 2047 rows, rank 64, with 32 / 64 / 128 rows in the second
-// product 118 / 84 / 136 us (operands of B read for each tile; registers); tiles
-// of 16 rows in the first one 2 - 7 % faster up to 1024 rows, 1 - 8 % slower from
-// 2047 on.
+// product 125 / 89 / 148 us (operands of B read for each tile; registers), 8191
+// rows of rank 16 78 / 72 / 84, though three matrices in f32 of 2047 rows 47 / 51 /
+// 56; tiles of 16 rows in the first one 2 - 7 % faster up to 1024 rows, and from
+// 2047 on between 1 % faster and 5 % slower.
 constexpr int kShort = 16, kLongShrink = 32, kLongExpand = 64;
 
 struct Tile {
@@ -559,7 +560,7 @@ LoraPlan lora_plan(int64_t M, int entries, int64_t C, int n, int r) {
   // column chunks until the compute units have two workgroups, none shorter
   // than two steps of every wave.  Long entries: at most four, which every
   // workgroup of the second product adds up again (2047 rows of gate and up,
-  // 14 chunks: 364 us, four: 109).
+  // rank 64: 15 chunks 100 us, four 89).
   const int64_t want = 4 * (int64_t)device_cus() / (p.shrink_slots ? p.shrink_slots : 1), most = p.few ? 32 : 4;
   int64_t splits = (C + 255) / 256;
   if (splits > want) splits = want;
