@@ -199,10 +199,10 @@ __global__ __launch_bounds__(kThreads, 2) void lora_shrink_kernel(LoraArgs a) {
 // for bf16 outputs also: where y or another rank's product cancels the rest,
 // the dropped bits are what is left (gate and up of 2047 rows, rank 64: 84.6 us
 // with two, 87.6 with three; 8191 rows, rank 16: 72.5 and 72.9).  The
-// contraction is (part, rank), in units of
-// eight ranks, four units a matrix instruction, and an operand of B serves all
-// parts.  MFMA row 4 g + e of instruction q is output 8 g + 4 q + e, so two
-// instructions leave eight neighbouring outputs of a row in a lane.
+// contraction is (part, rank), in units of eight ranks, four units a matrix
+// instruction, and an operand of B serves all parts.  MFMA row 4 g + e of
+// instruction q is output 8 g + 4 q + e, so two instructions leave eight
+// neighbouring outputs of a row in a lane.
 //
 // 32 rows of B are one stretch of memory; they are loaded as that and turned
 // into operands in LDS, a wave's own: unit k of row i lies at k ^ turn(i), which
@@ -551,9 +551,10 @@ LoraPlan lora_plan(int64_t M, int entries, int64_t C, int n, int r) {
   // and gate and up, 5120 -> 17408:
   //   rank 16, 64 of 1, 8: 31 / 37, 40 / 43;  rank 64, 16 of 1, 2, 8: 28 / 31,
   //   31 / 32, 69 / 33, but 64 of 1 84 / 68.
-  // A prompt among single tokens is cut as the mean says, which loses little:
-  // rank 16, 1000 + 255 x 1 56 / 63, 1000 + 63 x 1 30 / 29, 500 + 63 x 1 23 / 27;
-  // gate and up, rank 64, 4000 + 31 x 1 365 / 259, 500 + 255 x 1 292 / 349.
+  // A prompt among single tokens is cut as the mean says, up to a fifth slower than
+  // the other way: rank 16, 1000 + 255 x 1 56 / 63, 1000 + 63 x 1 30 / 29,
+  // 500 + 63 x 1 23 / 27; gate and up, rank 64, 4000 + 31 x 1 365 / 259, 500 + 255 x 1
+  // 292 / 349.
   p.few = M * r <= 128 * (int64_t)entries;
   p.shrink_slots = slots_of(M, entries, p.few ? kShort : kLongShrink);
   p.expand_slots = slots_of(M, entries, p.few ? kShort : kLongExpand);
